@@ -75,8 +75,9 @@ struct Record {
 };
 
 __device__ __forceinline__ Pair entry_log(const Record& rec, float v) {
-  const Pair x = two_sum(v, -rec.base) * rec.inv_t;
-  return fabsf(x.hi) < INFINITY ? x - rec.off : Pair{x.hi, 0.f};  // past float32's range: the pair's rest is void
+  // past float32's range a pair is void (an infinity less itself); a float32 product says so
+  const float far = __fmul_rn(v - rec.base, rec.inv_t.hi);
+  return fabsf(far) < 1e38f ? two_sum(v, -rec.base) * rec.inv_t - rec.off : Pair{far, 0.f};
 }
 
 // exp(x) of a pair, to float32 precision of the result.
