@@ -15,6 +15,7 @@
 // for a student that agrees with its teacher).  For loss and gradient at once the slice stays in shared memory
 // between the sums and the gradient: one read and one write of the row.
 #include <atomic>
+#include <cstddef>
 
 #include "../../include/spec_verify.h"
 #include "common.cuh"
@@ -173,12 +174,12 @@ struct Slice {
 // for three CTAs only, and their warps have to hide the loads (2048 x 128256: 254 us with 256, 282 with 128).
 __host__ __device__ constexpr int threads_of(bool grad) { return grad ? kDT : kDT / 2; }
 
-// What a CTA tells the others of its cluster.
-struct Part {
+// What a CTA tells the others of its cluster (pairs are stored as 8-byte vectors).
+struct __align__(8) Part {
   Pair rest, top;       // weights of its tokens outside and inside the record, relative to ref
-  Pair mass, against;   // over its tokens of the record: sum of p, of p (ln p - (s - ref0) / T)
-  float ref, ref0;
-  int flags;            // 1: a token twice, 2: a token with p > 0 has no weight in the student
+  Pair mass, against;   // over its tokens of the record: sum of p, of p (ln p - (s - ref) / T)
+  float ref;
+  int flags;            // 1: a token twice, 2: a token with p > 0 has the student's logit -inf
   float most;           // its largest logit (second pass only)
 };
 
@@ -192,12 +193,13 @@ struct Shared {
   int any;                           // the flags of the CTA's threads
 };
 
-// A token of the record that lies in this CTA's slice: its teacher's logit (then its probability), its student
-// logit.
-struct Entry {
-  float p, l;
+// A token of the record that lies in this CTA's slice: its teacher's logit and probability, its student logit.
+struct __align__(16) Entry {
+  float v, p, l;
   int id;
 };
+
+static_assert(sizeof(Part) % 8 == 0 && offsetof(Shared, parts) % 8 == 0, "pairs of every CTA's part lie on 8 bytes");
 
 __host__ __device__ constexpr int shared_bytes() { return (static_cast<int>(sizeof(Shared)) + 15) / 16 * 16; }
 
@@ -378,16 +380,30 @@ __device__ __forceinline__ void map_ends(const T* row, T* out, int V, const Slic
 
 // ---------------------------------------------------------------- loss, and loss with gradient
 
+// Where the first references are kept: a slice's sums below kFarSum, so that its weights lose nothing to the step to
+// the common reference, and a slice with mass of the record within kFarRef T of that, so that the loss's terms (some 45
+// bits) lose no more than 2^-30 to the change of reference.
+constexpr float kFarSum = 1073741824.f;  // 2^30
+constexpr float kFarRef = 16384.f;
+
 __device__ __forceinline__ void dsmem_st_pair(uint32_t addr, const Pair& v) { dsmem_st_v2(addr, v.hi, v.lo); }
 __device__ __forceinline__ void dsmem_st_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// 2^((from - to) c): what a sum relative to `from` is worth relative to `to`.
+// 2^((from - to) c): what a sum relative to `from` is worth relative to `to`.  (Nothing below float32's range: a pair
+// of so large a difference is void.)
 __device__ __forceinline__ float step(float from, float to, float c) {
+  if ((from - to) * c < -150.f) return 0.f;
   const Pair y = two_sum(from, -to) * Pair{c, 0.f};
   const float e = exp2f(y.hi);
   return __fmaf_rn(e, y.lo * kLn2Hi, e);
+}
+
+// a + b, a = m x for the float32 factors m and x: a pair past float32's range is void, and the product stands for it.
+__device__ __forceinline__ float shifted(float m, const Pair& x, const Pair& b) {
+  const float far = __fmul_rn(m, x.hi);
+  return fabsf(far) < INFINITY ? value(x * m + b) : far;
 }
 
 // The row's loss and statistics from its CTAs' parts, by one thread while the others go on to the gradient.
@@ -399,19 +415,21 @@ __device__ __noinline__ void write_loss(const DistillParams& p, int r, const Par
     const float f = step(parts[i].ref, most, c);
     rest = rest + parts[i].rest * f;
     inside = inside + parts[i].top * f;
+    if (!(value(parts[i].mass) > 0.f)) continue;  // (its reference may be anything)
     mass = mass + parts[i].mass;
-    loss = loss + (parts[i].against + parts[i].mass * (two_sum(most, -parts[i].ref0) * rec.inv_t));
+    loss = loss + (parts[i].against + parts[i].mass * (two_sum(most, -parts[i].ref) * rec.inv_t));
   }
   const bool some_rest = value(rest) > 0.f;
   const float tail = p.teacher_lse ? fmaxf(0.f, value(Pair{1.f, 0.f} - mass)) : 0.f;
-  const Pair ln = log_pair(rest + inside), shift = rec.inv_t * most;
+  const Pair ln = log_pair(rest + inside);
   const Pair ln_rest = some_rest ? log_pair(rest) : Pair{-INFINITY, 0.f};
   loss = loss + mass * ln;
   if (tail > 0.f && some_rest) loss = loss + (log_pair(Pair{tail, 0.f}) - ln_rest + ln) * tail;
   const bool infinite = (flags & 2) || (tail > 0.f && !some_rest), invalid = flags & 1;
-  p.loss[r] = invalid ? NAN : infinite ? INFINITY : value(loss);
-  p.stats[2 * r] = invalid ? NAN : value(shift + ln);
-  p.stats[2 * r + 1] = invalid ? NAN : some_rest ? value(shift + ln_rest) : -INFINITY;
+  // (a term past float32's range, of a masked token with p > 0, leaves a pair void: +inf)
+  p.loss[r] = invalid ? NAN : infinite || !(fabsf(value(loss)) < INFINITY) ? INFINITY : value(loss);
+  p.stats[2 * r] = invalid ? NAN : shifted(most, rec.inv_t, ln);
+  p.stats[2 * r + 1] = invalid ? NAN : some_rest ? shifted(most, rec.inv_t, ln_rest) : -INFINITY;
 }
 
 // Loss and statistics of a row, and its gradient (kGrad).  Bound: without the gradient the loads (eight CTAs per SM,
@@ -511,7 +529,6 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
   for (int w = 1; w < kW; ++w) ref = fmaxf(ref, sh.red[w]);
   if (!(fabsf(ref) < INFINITY)) ref = 0.f;
   const float c = p.c;
-  const float ref0 = ref;
   int n;  // entries of this slice
   {
     const int mine = sh.count[lane];  // kMaxTop / 32 = 32 runs of 32 entries
@@ -531,14 +548,14 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
       if (is) {
         const int k = i * kT + tid;
         entries[base + __popc(all & ((1u << lane) - 1u))] =
-            i == 0 ? Entry{v0, 0.f, id0} : Entry{values[k], 0.f, ids[k]};
+            i == 0 ? Entry{v0, 0.f, 0.f, id0} : Entry{values[k], 0.f, 0.f, ids[k]};
       }
     }
   }
   __syncthreads();
 
   int flags = bad ? 1 : 0;
-  // the sums relative to `ref`; again with the row's largest logit where the first reference was far off
+  // the sums relative to `ref`; again with the row's largest logit where a first reference was far off
   for (int again = 0;; ++again) {
     const Scale w(c, ref);
     flags |= twice;
@@ -550,33 +567,27 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
       Pair mass{0.f, 0.f}, against{0.f, 0.f}, top{0.f, 0.f};
       for (int i = tid; i < n; i += kT) {
         Entry e = entries[i];
-        if (again == 0) {
-          e.l = i < kT ? logit : Elems<T>::one(row, e.id);
-          const Pair x = entry_log(rec, e.p);
-          const bool some_p = e.p > -INFINITY;
-          e.p = some_p ? exp_pair(x) : 0.f;
-          entries[i] = e;
-          mass = mass + Pair{e.p, 0.f};
-          const Pair z = two_sum(e.l, -ref0) * rec.inv_t;
-          if (fabsf(z.hi) < INFINITY)
-            against = e.p > 0.f ? against + (x - z) * e.p : against;
+        if (again == 0) e.l = i < kT ? logit : Elems<T>::one(row, e.id);
+        const Pair x = entry_log(rec, e.v);
+        e.p = exp_pair(x);
+        if (again == 0) entries[i] = e;
+        mass = mass + Pair{e.p, 0.f};
+        if (e.p > 0.f) {  // (p before 1 / T: a masked logit times 1 / T may leave float32's range)
+          if (e.l > -INFINITY)
+            against = against + (x * e.p - two_sum(e.l, -ref) * e.p * rec.inv_t);
           else
-            flags |= e.p > 0.f ? 2 : 0;
+            flags |= 2;
         }
         top = top + Pair{w(e.l), 0.f};
       }
       top = w.clean(top);
-      if (again == 0) {
-        mass = warp_sum(mass);
-        against = warp_sum(against);
-      }
+      mass = warp_sum(mass);
+      against = warp_sum(against);
       top = warp_sum(top);
       if (lane == 0) {
         sh.part[1][warp] = top;
-        if (again == 0) {
-          sh.part[2][warp] = mass;
-          sh.part[3][warp] = against;
-        }
+        sh.part[2][warp] = mass;
+        sh.part[3][warp] = against;
       }
     } else if (lane < 3) {
       sh.part[1 + lane][warp] = Pair{0.f, 0.f};
@@ -597,9 +608,8 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
         const uint32_t there = dsmem_map(mine, cta) - mine;
         Part* to = &sh.parts[rank];
         Pair* place = which == 0 ? &to->rest : which == 1 ? &to->top : which == 2 ? &to->mass : &to->against;
-        if (which < 2 || again == 0) dsmem_st_pair(there + smem_addr(place), t);
+        dsmem_st_pair(there + smem_addr(place), t);
         if (which == 0) dsmem_st_f32(there + smem_addr(&to->ref), ref);
-        if (which == 1) dsmem_st_f32(there + smem_addr(&to->ref0), ref0);
         if (which == 2) dsmem_st_u32(there + smem_addr(&to->flags), static_cast<uint32_t>(sh.any));
       }
       __syncwarp();
@@ -618,6 +628,9 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
         any |= __shfl_xor_sync(0xffffffffu, any, o);
       }
+      // a slice whose sums left its first loads far below, or whose record is far from them
+      const bool far = !(value(part.rest + part.top) < kFarSum) ||
+                       (value(part.mass) > 0.f && !((most - part.ref) * p.inv_t < kFarRef));
       const float f = step(part.ref, most, c);
       float rest = value(part.rest) * f, total = value(part.rest + part.top) * f, mass = value(part.mass);
 #pragma unroll 1
@@ -638,13 +651,16 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
         sh.k_out = (any & 1) ? NAN : (both - share) * k;
         sh.most = most;
         sh.flags = any;
-        sh.again = !again && !(any & 1) && !(total < 1.2676506e30f && total > 8.6736174e-19f);  // 2^100, 2^-60
       }
+      const bool redo = __any_sync(0xffffffffu, far) || !(total > 8.6736174e-19f);  // 2^-60
+      if (lane == 0) sh.again = !again && !(any & 1) && redo;
     }
     __syncthreads();
     flags = sh.flags;
     if (!sh.again) break;
     // out of range (or NaN): the largest logit of the slice, then of the row
+    flags &= 1;
+    if (tid == 0) sh.any = 0;
     float m = -INFINITY;
     const uint4* r4 = reinterpret_cast<const uint4*>(row + s.head) + s.v0;
     for (int v = tid; v < s.v1 - s.v0; v += kT) {

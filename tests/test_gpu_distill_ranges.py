@@ -106,6 +106,9 @@ def batch(N, V, K, dtype, T, seed, sigma=2.5):
     return student.to(torch.bfloat16 if dtype == "bf16" else torch.float32), v.contiguous(), i.to(torch.int32), lse
 
 
+ROWS = pytest.mark.parametrize("N,V", [(1, 70000), (3, 20000), (700, 20000), (340, 70001)])  # eight to one CTA per row
+
+
 @pytest.mark.parametrize("T", [0.5, 1.0, 1.3])
 def test_record_values_of_the_types_lowest_value(S, T):
     # a teacher whose vocabulary is masked by a finite value and whose record is longer than what is left
@@ -114,3 +117,24 @@ def test_record_values_of_the_types_lowest_value(S, T):
     v[3, 1:] = MIN
     for l in (lse, None):
         check(S, student, v, i, T, l)
+
+
+@ROWS
+@pytest.mark.parametrize("T", [0.5, 1.0, 1.3])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("mask", ["lowest", -1e30, -1e12, -1e4, -float("inf")])
+def test_masked_first_logits(S, N, V, T, dtype, mask):
+    student, v, i, lse = batch(N, V, 30, dtype, T, 50)
+    mask = torch.finfo(student.dtype).min if mask == "lowest" else mask
+    # the row's start, the start of its second half (a slice's of any number of CTAs), all but its end
+    for a, b in ((0, 8192 + 100), (V // 2 - 8, V // 2 + 8200), (0, V - 300)):
+        x = student.clone()
+        x[:, a:b] = mask
+        outside = (i < a) | (i >= b)
+        ids = torch.where(outside, i, -1)   # the teacher's tokens of the masked run left out
+        ids[:, 0] = torch.where(outside.any(1), ids[:, 0], V - 1)
+        rows = [0, N // 2, N - 1]
+        for l in (lse, None):
+            check(S, x, v, ids, T, l, rows)
+            if mask > -1e9:  # and left in: their logits are the masked ones
+                check(S, x, v, i, T, l, rows)
