@@ -344,9 +344,10 @@ int spec_top_logits(const void* logits, int dtype, float temperature, int R, int
  *    outside the record: loss = sum_i p_i ln(p_i / q_i) + r ln(r / Q_rest).
  *  - teacher_lse NULL: p is the softmax of the record's values / T, and loss = sum_i p_i ln(p_i / q_i).
  * A term with p_i = 0 (or r = 0) is 0; a token with p_i > 0 whose student logit
- * is -inf makes the loss +inf.  Sums are float32, compensated; a weight more than
- * 87 below its neighbourhood's largest in the logarithm (logits 87 T apart) counts
- * as 0.
+ * is -inf makes the loss +inf.  Sums are float32, compensated; those over the
+ * record's tokens and over the others are taken apart however far their logits
+ * lie from one another, and in each a weight more than 87 below the largest in the
+ * logarithm (logits 87 T apart) may count as 0.
  *
  *   student    [N, V]  dtype
  *   values     [N, K]  float32: the record's logits (-inf allowed: p_i = 0; entries with id -1 are not read

@@ -8,10 +8,10 @@
 //             (m + r - r / Q_rest) q_j     for any other, Q_rest = exp(lse_rest - lse), q_j = exp(z_j - lse).
 //
 // A cluster of CTAs takes a row, each its slice, and reads it once.  Weights are 2^((s - R) log2(e) / T) with R the
-// largest of the slice's first loads, so that nothing is rescaled on the way; a sum that leaves float32's range for
-// a reference that is far off
-// (logits sorted upwards, masked runs) is taken again relative to the row's largest logit.  The tail is summed
-// by itself, a bitmap of the record's tokens keeping them out (the whole sum less the record's would cancel
+// largest of the slice's first loads, so that nothing is rescaled on the way.  Where such references are far off
+// (logits sorted upwards, masked runs, a student that gives the record all but 2^-60 of its mass), the sums are taken
+// again, over the record and over the rest relative to the largest logit of each, so that neither leaves float32's
+// range however far the two lie apart.  The tail is summed by itself, a bitmap of the record's tokens keeping them out (the whole sum less the record's would cancel
 // for a student that agrees with its teacher).  For loss and gradient at once the slice stays in shared memory
 // between the sums and the gradient: one read and one write of the row.
 #include <atomic>
@@ -176,11 +176,12 @@ __host__ __device__ constexpr int threads_of(bool grad) { return grad ? kDT : kD
 
 // What a CTA tells the others of its cluster (pairs are stored as 8-byte vectors).
 struct __align__(8) Part {
-  Pair rest, top;       // weights of its tokens outside and inside the record, relative to ref
+  Pair rest, top;       // weights of its tokens outside and inside the record, relative to its first loads' largest
+                        // logit; in the second pass to the row's largest outside, and inside
   Pair mass, against;   // over its tokens of the record: sum of p, of p (ln p - (s - ref) / T)
-  float ref;
+  float ref;            // its first loads' largest logit; in the second pass the row's largest
   int flags;            // 1: a token twice, 2: a token with p > 0 has the student's logit -inf
-  float most;           // its largest logit (second pass only)
+  float out, in;        // its largest logits outside and inside (second pass only)
 };
 
 struct Shared {
@@ -188,6 +189,7 @@ struct Shared {
   Pair part[4][kDW];
   int count[kMaxTop / 32];
   Part parts[kDSplit];
+  float ref, ref_out, ref_in;        // the references of Part::against, rest and top
   float most, k_in, k_out;           // the largest of the references; what a weight is worth in the gradient
   int flags, again;
   int any;                           // the flags of the CTA's threads
@@ -380,11 +382,13 @@ __device__ __forceinline__ void map_ends(const T* row, T* out, int V, const Slic
 
 // ---------------------------------------------------------------- loss, and loss with gradient
 
-// Where the first references are kept: a slice's sums below kFarSum, so that its weights lose nothing to the step to
+// Where the first references are kept: the tail's sum at least kLeastRest, so that the weights that are 0 (below 2^-126)
+// are nothing to it and its quotients stay in range; a slice's sums below kFarSum, so that its weights lose nothing to the step to
 // the common reference, and a slice with mass of the record within kFarRef T of that, so that the loss's terms (some 45
 // bits) lose no more than 2^-30 to the change of reference.
 constexpr float kFarSum = 1073741824.f;  // 2^30
 constexpr float kFarRef = 16384.f;
+constexpr float kLeastRest = 8.6736174e-19f;  // 2^-60
 
 __device__ __forceinline__ void dsmem_st_pair(uint32_t addr, const Pair& v) { dsmem_st_v2(addr, v.hi, v.lo); }
 __device__ __forceinline__ void dsmem_st_u32(uint32_t addr, uint32_t v) {
@@ -406,13 +410,66 @@ __device__ __forceinline__ float shifted(float m, const Pair& x, const Pair& b) 
   return fabsf(far) < INFINITY ? value(x * m + b) : far;
 }
 
-// The row's loss and statistics from its CTAs' parts, by one thread while the others go on to the gradient.
-__device__ __noinline__ void write_loss(const DistillParams& p, int r, const Part* parts, int split, const Record& rec,
-                                        float most, float c, int flags) {
+// The largest logits of a slice outside its record's tokens and of those tokens (NaN and +inf stand out), and from them,
+// over the cluster, the row's; they become the references (sh.ref, sh.ref_out, sh.ref_in).  0: the row is invalid, 1:
+// it has nothing but -inf outside the record, 2: the rest.  (A function of its own for its registers' sake.)
+template <typename T, int kT>
+__device__ __noinline__ int own_references(const T* row, int V, const Slice<T>& s, const uint32_t* bits,
+                                           const Entry* entries, int n, int rank, int split, Shared& sh) {
+  constexpr int kV = Elems<T>::kVec;
+  const int tid = threadIdx.x;
+  const uint4* r4 = reinterpret_cast<const uint4*>(row + s.head) + s.v0;
+  float out = -INFINITY, in = -INFINITY;
+  for (int v = tid; v < s.v1 - s.v0; v += kT) {
+    const uint32_t listed = bits[v * kV / 32] >> (v * kV % 32);
+    float f[kV];
+    Elems<T>::widen(ldg_stream(r4 + v), f);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) out = (listed >> j) & 1u ? out : max_nan(out, f[j]);
+  }
+  auto one = [&](int id, int bit) {
+    if (!((bits[bit >> 5] >> (bit & 31)) & 1u)) out = max_nan(out, Elems<T>::one(row, id));
+  };
+  if (s.first && tid < s.head) one(tid, s.per * kV + tid);
+  if (s.last && tid < V - s.head - s.nv * kV) one(s.head + s.nv * kV + tid, s.per * kV + 8 + tid);
+  for (int i = tid; i < n; i += kT) in = max_nan(in, entries[i].l);
+  out = block_max<kT>(out, sh.red);
+  in = block_max<kT>(in, sh.red);
+  if (tid < split) {
+    const uint32_t mine = smem_addr(&sh), there = dsmem_map(mine, tid) - mine;
+    dsmem_st_f32(there + smem_addr(&sh.parts[rank].out), out);
+    dsmem_st_f32(there + smem_addr(&sh.parts[rank].in), in);
+  }
+  __syncwarp();
+  if (split > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  for (int i = 0; i < split; ++i) {
+    out = max_nan(out, sh.parts[i].out);
+    in = max_nan(in, sh.parts[i].in);
+  }
+  const float most = max_nan(out, in);
+  if (tid == 0) {
+    sh.any = 0;
+    sh.ref = most;
+    sh.ref_out = out > -INFINITY ? out : most;  // (nothing is there to be summed)
+    sh.ref_in = in > -INFINITY ? in : most;
+  }
+  __syncthreads();
+  return !(fabsf(most) < INFINITY) ? 0 : out > -INFINITY ? 2 : 1;
+}
+
+// The row's loss and statistics from its CTAs' parts, by one thread while the others go on to the gradient.  again: of
+// the second pass.
+__device__ __noinline__ void write_loss(const DistillParams& p, int r, const Shared& sh, int split, const Record& rec,
+                                        float c, int flags, int again) {
+  const Part* parts = sh.parts;
+  const float most = sh.most, ref_out = again ? sh.ref_out : most;
   Pair rest{0.f, 0.f}, inside{0.f, 0.f}, mass{0.f, 0.f}, loss{0.f, 0.f};
 #pragma unroll 1
   for (int i = 0; i < split; ++i) {
-    const float f = step(parts[i].ref, most, c);
+    const float f = again ? 1.f : step(parts[i].ref, most, c);
     rest = rest + parts[i].rest * f;
     inside = inside + parts[i].top * f;
     if (!(value(parts[i].mass) > 0.f)) continue;  // (its reference may be anything)
@@ -421,15 +478,16 @@ __device__ __noinline__ void write_loss(const DistillParams& p, int r, const Par
   }
   const bool some_rest = value(rest) > 0.f;
   const float tail = p.teacher_lse ? fmaxf(0.f, value(Pair{1.f, 0.f} - mass)) : 0.f;
-  const Pair ln = log_pair(rest + inside);
+  const Pair ln = log_pair(again ? rest * step(ref_out, most, c) + inside * step(sh.ref_in, most, c) : rest + inside);
   const Pair ln_rest = some_rest ? log_pair(rest) : Pair{-INFINITY, 0.f};
   loss = loss + mass * ln;
-  if (tail > 0.f && some_rest) loss = loss + (log_pair(Pair{tail, 0.f}) - ln_rest + ln) * tail;
+  if (tail > 0.f && some_rest)
+    loss = loss + ((log_pair(Pair{tail, 0.f}) - ln_rest + ln) * tail + two_sum(most, -ref_out) * tail * rec.inv_t);
   const bool infinite = (flags & 2) || (tail > 0.f && !some_rest), invalid = flags & 1;
   // (a term past float32's range, of a masked token with p > 0, leaves a pair void: +inf)
   p.loss[r] = invalid ? NAN : infinite || !(fabsf(value(loss)) < INFINITY) ? INFINITY : value(loss);
   p.stats[2 * r] = invalid ? NAN : shifted(most, rec.inv_t, ln);
-  p.stats[2 * r + 1] = invalid ? NAN : some_rest ? shifted(most, rec.inv_t, ln_rest) : -INFINITY;
+  p.stats[2 * r + 1] = invalid ? NAN : some_rest ? shifted(ref_out, rec.inv_t, ln_rest) : -INFINITY;
 }
 
 // Loss and statistics of a row, and its gradient (kGrad).  Bound: without the gradient the loads (eight CTAs per SM,
@@ -528,6 +586,7 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
 #pragma unroll
   for (int w = 1; w < kW; ++w) ref = fmaxf(ref, sh.red[w]);
   if (!(fabsf(ref) < INFINITY)) ref = 0.f;
+  if (tid == 0) sh.ref = sh.ref_out = sh.ref_in = ref;
   const float c = p.c;
   int n;  // entries of this slice
   {
@@ -554,16 +613,19 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
   }
   __syncthreads();
 
-  int flags = bad ? 1 : 0;
-  // the sums relative to `ref`; again with the row's largest logit where a first reference was far off
-  for (int again = 0;; ++again) {
+  int flags = bad ? 1 : 0, again = 0, some_rest = 1;
+  // the sums relative to the slice's reference; again with the row's own where those were far off
+  for (;; again = 1) {
     const Scale w(c, ref);
     flags |= twice;
     // the first entry's logit is on its way while the slice is streamed
     const float logit = again == 0 && tid < n ? Elems<T>::one(row, entries[tid].id) : 0.f;
     if (kGrad && again == 0) kept_wait<0>();
-    const Pair sum = warp_sum(w.clean(sum_slice<T, kT, kGrad>(row, p.V, s, bits, hits, first, w, kept)));
+    Pair sum{0.f, 0.f};
+    if (some_rest) sum = warp_sum(w.clean(sum_slice<T, kT, kGrad>(row, p.V, s, bits, hits, first, w, kept)));
     if (warp * 32 < n) {
+      const float ref = sh.ref;
+      const Scale w(c, sh.ref_in);
       Pair mass{0.f, 0.f}, against{0.f, 0.f}, top{0.f, 0.f};
       for (int i = tid; i < n; i += kT) {
         Entry e = entries[i];
@@ -609,7 +671,7 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
         Part* to = &sh.parts[rank];
         Pair* place = which == 0 ? &to->rest : which == 1 ? &to->top : which == 2 ? &to->mass : &to->against;
         dsmem_st_pair(there + smem_addr(place), t);
-        if (which == 0) dsmem_st_f32(there + smem_addr(&to->ref), ref);
+        if (which == 0) dsmem_st_f32(there + smem_addr(&to->ref), sh.ref);
         if (which == 2) dsmem_st_u32(there + smem_addr(&to->flags), static_cast<uint32_t>(sh.any));
       }
       __syncwarp();
@@ -631,8 +693,10 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
       // a slice whose sums left its first loads far below, or whose record is far from them
       const bool far = !(value(part.rest + part.top) < kFarSum) ||
                        (value(part.mass) > 0.f && !((most - part.ref) * p.inv_t < kFarRef));
-      const float f = step(part.ref, most, c);
-      float rest = value(part.rest) * f, total = value(part.rest + part.top) * f, mass = value(part.mass);
+      const float f_out = step(again ? sh.ref_out : part.ref, most, c);
+      const float f_in = again ? step(sh.ref_in, most, c) : f_out;
+      float rest = value(part.rest) * (again ? 1.f : f_out), mass = value(part.mass);
+      float total = again ? value(part.rest) * f_out + value(part.top) * f_in : value(part.rest + part.top) * f_out;
 #pragma unroll 1
       for (int o = 1; o < split; o <<= 1) {
         rest += __shfl_xor_sync(0xffffffffu, rest, o);
@@ -640,60 +704,38 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
         mass += __shfl_xor_sync(0xffffffffu, mass, o);
       }
       if (lane == rank) {
-        // q = weight f / total, f the step from this CTA's reference to the common one
+        // a token of the record has q = weight f_in / total, f_in the step from its reference to the common one; any
+        // other weighs f_out / total in the row and f / rest in the tail
         const float tail = p.teacher_lse ? fmaxf(0.f, 1.f - mass) : 0.f, both = mass + tail;
         // (approximate quotients, two steps of 2^-23: their operands' weights carry the exponential's 2^-22 each)
-        float share = 0.f;
-        if (tail > 0.f && rest > 0.f)
-          share = __fmul_rn(tail, rest > 1e-30f ? __fdividef(total, rest) : __fdiv_rn(total, rest));
-        const float k = __fdividef(__fmul_rn(__fmul_rn(__fmul_rn(g, p.inv_t), f), 1.f - w.miss), total);
-        sh.k_in = both * k;
-        sh.k_out = (any & 1) ? NAN : (both - share) * k;
+        const float scale = __fmul_rn(g, p.inv_t), f = again ? 1.f : f_out;
+        const float share = tail > 0.f && rest > 0.f ? __fdividef(__fmul_rn(tail, f), rest) : 0.f;
+        sh.k_in = __fdividef(__fmul_rn(both, f_in), total) * __fmul_rn(scale, 1.f - Scale(c, sh.ref_in).miss);
+        sh.k_out = (any & 1) ? NAN : (__fdividef(__fmul_rn(both, f_out), total) - share) * __fmul_rn(scale, 1.f - w.miss);
         sh.most = most;
         sh.flags = any;
       }
-      const bool redo = __any_sync(0xffffffffu, far) || !(total > 8.6736174e-19f);  // 2^-60
+      const bool redo = __any_sync(0xffffffffu, far) || !(rest >= kLeastRest);
       if (lane == 0) sh.again = !again && !(any & 1) && redo;
     }
     __syncthreads();
     flags = sh.flags;
     if (!sh.again) break;
-    // out of range (or NaN): the largest logit of the slice, then of the row
     flags &= 1;
-    if (tid == 0) sh.any = 0;
-    float m = -INFINITY;
-    const uint4* r4 = reinterpret_cast<const uint4*>(row + s.head) + s.v0;
-    for (int v = tid; v < s.v1 - s.v0; v += kT) {
-      float f[kV];
-      Elems<T>::widen(ldg_stream(r4 + v), f);
-#pragma unroll
-      for (int j = 0; j < kV; ++j) m = max_nan(m, f[j]);
-    }
-    if (s.first && tid < s.head) m = max_nan(m, Elems<T>::one(row, tid));
-    if (s.last && s.head + s.nv * kV + tid < p.V) m = max_nan(m, Elems<T>::one(row, s.head + s.nv * kV + tid));
-    m = block_max<kT>(m, sh.red);
-    if (tid < split) {
-      const uint32_t mine = smem_addr(&sh), there = dsmem_map(mine, tid) - mine;
-      dsmem_st_f32(there + smem_addr(&sh.parts[rank].most), m);
-    }
-    __syncwarp();
-    if (split > 1)
-      cluster_sync();
-    else
-      __syncthreads();
-    ref = sh.parts[0].most;
-    for (int i = 1; i < split; ++i) ref = max_nan(ref, sh.parts[i].most);
-    if (!(fabsf(ref) < INFINITY)) {  // NaN or +inf in the row, or nothing but -inf
+    const int found = own_references<T, kT>(row, p.V, s, bits, entries, n, rank, split, sh);
+    if (found == 0) {  // NaN or +inf in the row, or nothing but -inf
       flags |= 1;
       if (tid == 0) sh.k_out = NAN;
       __syncthreads();
       break;
     }
-    if (!kGrad) first_loads<T, kT>(row, s, first);
+    ref = sh.ref_out;
+    some_rest = found == 2;
+    if (!kGrad && some_rest) first_loads<T, kT>(row, s, first);
   }
 
   const bool invalid = flags & 1;
-  if (rank == 0 && tid == kT - 1) write_loss(p, r, sh.parts, split, rec, sh.most, c, flags);
+  if (rank == 0 && tid == kT - 1) write_loss(p, r, sh, split, rec, c, flags, again);
   if (!kGrad) return;
   if (g == 0.f) {
     zero_slice<T, kT>(out, p.V, s, p.vec != 0);
@@ -708,9 +750,10 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
   if (invalid) return;
   __syncthreads();
   // the slice's tokens of the record, over what was written there
+  const Scale w_in(c, sh.ref_in);
   for (int i = tid; i < n; i += kT) {
     const Entry e = entries[i];
-    out[e.id] = to_grad<T>(__fmaf_rn(w(e.l), k_in, -__fmul_rn(e.p, scale)));
+    out[e.id] = to_grad<T>(__fmaf_rn(w_in(e.l), k_in, -__fmul_rn(e.p, scale)));
   }
 }
 
@@ -762,14 +805,24 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   bad = __syncthreads_or(bad);
   const float tail = p.teacher_lse ? fmaxf(0.f, value(Pair{1.f, 0.f} - mass)) : 0.f;
   const float both = value(mass + Pair{tail, 0.f}), scale = __fmul_rn(g, rec.inv_t.hi);
-  const float share = tail > 0.f && lse_rest > -INFINITY ? tail * exp_pair(two_sum(lse, -lse_rest)) : 0.f;
-  // q = 2^(s c + shift), shift the float32 nearest to -T lse c; what the roundings of it and of T lse miss goes
+  // weights 2^(s c + shift), shift the float32 nearest to -T lse c; what the roundings of it and of T lse miss goes
   // into the factors
-  const float ref = __fmul_rn(lse, p.temperature);
-  const Scale w(p.c, ref);
-  const float off = __fmul_rn(__fmaf_rn(lse, p.temperature, -ref), p.inv_t);  // lse - ref / T
-  const float k = 1.f - (w.miss + off);
-  const float k_in = both * scale * k, k_out = bad ? NAN : (both - share) * scale * k;
+  auto scale_of = [&](float lse, float& k) {
+    const float ref = __fmul_rn(lse, p.temperature);
+    const Scale w(p.c, ref);
+    k = scale * (1.f - (w.miss + __fmul_rn(__fmaf_rn(lse, p.temperature, -ref), p.inv_t)));  // (lse - ref / T)
+    return w;
+  };
+  // tokens outside the record: q less their share of the tail, relative to lse, or to lse_rest where that is so far
+  // below that q is nothing and the quotient of the two would leave float32's range
+  const float gap = lse - lse_rest;
+  const bool apart = gap > 40.f && gap < INFINITY;
+  const float ratio = exp_pair(two_sum(apart ? lse_rest : lse, apart ? -lse : -lse_rest));
+  const float share = tail > 0.f && lse_rest > -INFINITY ? tail * (apart ? 1.f : ratio) : 0.f;
+  float k_in, k;
+  const Scale w_in = scale_of(lse, k_in), w = scale_of(apart ? lse_rest : lse, k);
+  k_in *= both;
+  const float k_out = bad ? NAN : (both * (apart ? ratio : 1.f) - share) * k;
   T* body = out + s.head;
   const bool vec = p.vec != 0;
   while (v < s.v1) {
@@ -786,7 +839,7 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
     const int id = ids[k];
     if (id < 0 || s.bit(id) < 0) continue;
     const float pk = values[k] > -INFINITY ? exp_pair(entry_log(rec, values[k])) : 0.f;
-    out[id] = to_grad<T>(__fmaf_rn(w(Elems<T>::one(row, id)), k_in, -__fmul_rn(pk, scale)));
+    out[id] = to_grad<T>(__fmaf_rn(w_in(Elems<T>::one(row, id)), k_in, -__fmul_rn(pk, scale)));
   }
 }
 

@@ -138,3 +138,33 @@ def test_masked_first_logits(S, N, V, T, dtype, mask):
             check(S, x, v, ids, T, l, rows)
             if mask > -1e9:  # and left in: their logits are the masked ones
                 check(S, x, v, i, T, l, rows)
+
+
+@ROWS
+@pytest.mark.parametrize("T", [0.25, 1.0])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_student_all_but_certain_of_the_record(S, N, V, T, dtype):
+    # the mass outside the record is e^-peak of the whole
+    student, v, i, lse = batch(N, V, 1, dtype, T, 52)
+    lse = (v[:, 0].double() / T - np.log(0.9)).float()  # the teacher's tail is 0.1
+    rows = sorted({0, N - 1})
+    for noise in (0.0, 1.0):
+        for peak in (30, 41, 60, 80, 87, 88, 90, 95, 99, 100, 102, 105, 130, 300, 4000):
+            x = student * noise
+            x.scatter_(1, i.long(), float(peak) * T)
+            check(S, x, v, i, T, lse, rows)
+            # statistics made in 64 bits
+            z = x[rows].double() / T
+            out = z.scatter(1, i[rows].long(), -float("inf"))
+            stats = torch.stack([torch.logsumexp(z, 1), torch.logsumexp(out, 1)], 1).float()
+            pick = [t[rows].contiguous() for t in (x, v, i, lse)]
+            check(S, pick[0], pick[1], pick[2], T, pick[3], None, stats)
+
+
+@ROWS
+def test_record_far_below_the_rest(S, N, V):
+    for T, low in ((1.0, -150.0), (0.3, -500.0), (1.0, -1e6)):
+        student, v, i, lse = batch(N, V, 20, "f32", T, 54)
+        student.scatter_(1, i.long(), low)
+        for l in (lse, None):
+            check(S, student, v, i, T, l, [0, N - 1])
