@@ -87,6 +87,16 @@ __device__ __forceinline__ float exp_pair(const Pair& x) {
   return fabsf(x.hi) < INFINITY ? __fmaf_rn(e, x.lo, e) : e;
 }
 
+// exp(x) of a pair, to some 2^-38 of itself: the teacher's mass beyond the record is what these leave of 1.
+__device__ __forceinline__ Pair probability(const Pair& x) {
+  const Pair y = x * Pair{1.44269502162933349609375f, 1.925963033500e-08f};
+  if (!(fabsf(y.hi) < 120.f)) return Pair{exp_pair(x), 0.f};
+  const float k = __fadd_rn(y.hi, 12582912.f);
+  const Pair e = exp2_near<false>(__fsub_rn(y.hi, __fsub_rn(k, 12582912.f))) * Pair{1.f, __fmul_rn(y.lo, kLn2Hi)};
+  const float scale = __int_as_float((127 + __float_as_int(k) - 0x4b400000) << 23);
+  return Pair{e.hi * scale, e.lo * scale};
+}
+
 template <int kT>
 __device__ __forceinline__ Pair block_sum(Pair v, Pair* part) {
   v = warp_sum(v);
@@ -631,12 +641,13 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
         Entry e = entries[i];
         if (again == 0) e.l = i < kT ? logit : Elems<T>::one(row, e.id);
         const Pair x = entry_log(rec, e.v);
-        e.p = exp_pair(x);
+        const Pair pr = probability(x);
+        e.p = value(pr);
         if (again == 0) entries[i] = e;
-        mass = mass + Pair{e.p, 0.f};
+        mass = mass + pr;
         if (e.p > 0.f) {  // (p before 1 / T: a masked logit times 1 / T may leave float32's range)
           if (e.l > -INFINITY)
-            against = against + (x * e.p - two_sum(e.l, -ref) * e.p * rec.inv_t);
+            against = against + (x * pr - two_sum(e.l, -ref) * pr * rec.inv_t);
           else
             flags |= 2;
         }
@@ -681,7 +692,8 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
     else
       __syncthreads();
     if (warp == 0) {
-      // lane i takes CTA i's part, relative to the largest of the references; float32 will do for the gradient
+      // lane i takes CTA i's part, relative to the largest of the references; float32 will do for the gradient, but for
+      // what the record's mass leaves of 1
       const Part& part = sh.parts[lane < split ? lane : 0];
       float most = part.ref;
       int any = part.flags;
@@ -694,29 +706,35 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
       const bool far = !(value(part.rest + part.top) < kFarSum) ||
                        (value(part.mass) > 0.f && !((most - part.ref) * p.inv_t < kFarRef));
       const float f_out = step(again ? sh.ref_out : part.ref, most, c);
-      const float f_in = again ? step(sh.ref_in, most, c) : f_out;
-      float rest = value(part.rest) * (again ? 1.f : f_out), mass = value(part.mass);
-      float total = again ? value(part.rest) * f_out + value(part.top) * f_in : value(part.rest + part.top) * f_out;
+      float rest = value(part.rest) * (again ? 1.f : f_out);
 #pragma unroll 1
-      for (int o = 1; o < split; o <<= 1) {
-        rest += __shfl_xor_sync(0xffffffffu, rest, o);
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-        mass += __shfl_xor_sync(0xffffffffu, mass, o);
-      }
-      if (lane == rank) {
+      for (int o = 1; o < split; o <<= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+      if (kGrad) {
+        const float f_in = again ? step(sh.ref_in, most, c) : f_out;
+        float total = again ? value(part.rest) * f_out + value(part.top) * f_in : value(part.rest + part.top) * f_out;
+        Pair mass = part.mass;
+#pragma unroll 1
+        for (int o = 1; o < split; o <<= 1) {
+          total += __shfl_xor_sync(0xffffffffu, total, o);
+          mass = mass + Pair{__shfl_xor_sync(0xffffffffu, mass.hi, o), __shfl_xor_sync(0xffffffffu, mass.lo, o)};
+        }
         // a token of the record has q = weight f_in / total, f_in the step from its reference to the common one; any
         // other weighs f_out / total in the row and f / rest in the tail
-        const float tail = p.teacher_lse ? fmaxf(0.f, 1.f - mass) : 0.f, both = mass + tail;
+        const float tail = p.teacher_lse ? fmaxf(0.f, value(Pair{1.f, 0.f} - mass)) : 0.f, both = value(mass) + tail;
         // (approximate quotients, two steps of 2^-23: their operands' weights carry the exponential's 2^-22 each)
         const float scale = __fmul_rn(g, p.inv_t), f = again ? 1.f : f_out;
         const float share = tail > 0.f && rest > 0.f ? __fdividef(__fmul_rn(tail, f), rest) : 0.f;
-        sh.k_in = __fdividef(__fmul_rn(both, f_in), total) * __fmul_rn(scale, 1.f - Scale(c, sh.ref_in).miss);
-        sh.k_out = (any & 1) ? NAN : (__fdividef(__fmul_rn(both, f_out), total) - share) * __fmul_rn(scale, 1.f - w.miss);
-        sh.most = most;
-        sh.flags = any;
+        if (lane == rank) {
+          sh.k_in = __fdividef(__fmul_rn(both, f_in), total) * __fmul_rn(scale, 1.f - Scale(c, sh.ref_in).miss);
+          sh.k_out = (any & 1) ? NAN : (__fdividef(__fmul_rn(both, f_out), total) - share) * __fmul_rn(scale, 1.f - w.miss);
+        }
       }
       const bool redo = __any_sync(0xffffffffu, far) || !(rest >= kLeastRest);
-      if (lane == 0) sh.again = !again && !(any & 1) && redo;
+      if (lane == 0) {
+        sh.most = most;
+        sh.flags = any;
+        sh.again = !again && !(any & 1) && redo;
+      }
     }
     __syncthreads();
     flags = sh.flags;
@@ -799,7 +817,7 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   const Record rec = read_record<kDT>(p, r, teacher_lse, red, part, &bad);
   Pair mass{0.f, 0.f};
   for (int k = tid; k < p.K; k += kDT)
-    if (ids[k] >= 0 && values[k] > -INFINITY) mass = mass + Pair{exp_pair(entry_log(rec, values[k])), 0.f};
+    if (ids[k] >= 0 && values[k] > -INFINITY) mass = mass + probability(entry_log(rec, values[k]));
   mass = block_sum<kDT>(mass, part);
   bad |= !(fabsf(lse) < INFINITY);  // the forward pass found the row invalid
   bad = __syncthreads_or(bad);
@@ -838,7 +856,7 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   for (int k = tid; k < p.K; k += kDT) {  // the slice's tokens of the record, over what was written there
     const int id = ids[k];
     if (id < 0 || s.bit(id) < 0) continue;
-    const float pk = values[k] > -INFINITY ? exp_pair(entry_log(rec, values[k])) : 0.f;
+    const float pk = values[k] > -INFINITY ? value(probability(entry_log(rec, values[k]))) : 0.f;
     out[id] = to_grad<T>(__fmaf_rn(w_in(Elems<T>::one(row, id)), k_in, -__fmul_rn(pk, scale)));
   }
 }

@@ -51,13 +51,16 @@ __device__ __forceinline__ Pair warp_sum(Pair v) {
   return v;
 }
 
-// 2^y for |y| <= 0.51 to 2^-40, by the table and polynomial of weight.cuh.
+// 2^y for |y| <= 0.51 to 2^-40, by the table and polynomial of weight.cuh.  kOne: called by one thread of a warp, the
+// table in constant memory (which serves one address at a time); else in global memory.
+template <bool kOne>
 __device__ __forceinline__ Pair exp2_near(float y) {
   const float k = __fmaf_rn(y, 64.f, 12582912.f);
   const int m = __float_as_int(k) - 0x4b400000;
   const float s = __fmaf_rn(__fsub_rn(k, 12582912.f), -0.015625f, y);
   const float scale = m < 0 ? 0.5f : 1.f;  // m in [-33, 33]
-  const Pair T{kExp2Table.hi[m & 63] * scale, kExp2Table.lo[m & 63] * scale};
+  const Exp2Table& tab = kOne ? kExp2Table : kExp2TableGlobal;
+  const Pair T{tab.hi[m & 63] * scale, tab.lo[m & 63] * scale};
   const float t = __fmul_rn(s, kLn2Hi);
   const float tl = __fmaf_rn(s, kLn2Hi, -t) + __fmul_rn(s, kLn2Lo);
   const float q = __fmul_rn(__fmul_rn(t, t), __fmaf_rn(t, __fmaf_rn(t, 1.f / 24.f, 1.f / 6.f), 0.5f));
@@ -72,7 +75,7 @@ __device__ __forceinline__ Pair log_pair(const Pair& s) {
   const float down1 = __int_as_float((127 - n / 2) << 23), down2 = __int_as_float((127 - (n - n / 2)) << 23);
   const Pair f{s.hi * down1 * down2, s.lo * down1 * down2};
   const float y = log2f(f.hi);
-  const Pair d = f * exp2_near(-y) - Pair{1.f, 0.f};
+  const Pair d = f * exp2_near<true>(-y) - Pair{1.f, 0.f};
   const float miss = __fadd_rn(d.hi, __fadd_rn(d.lo, -0.5f * d.hi * d.hi));
   return Pair{kLn2Hi, kLn2Lo} * static_cast<float>(n) + (Pair{kLn2Hi, kLn2Lo} * y + Pair{miss, 0.f});
 }

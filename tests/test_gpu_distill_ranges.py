@@ -168,3 +168,23 @@ def test_record_far_below_the_rest(S, N, V):
         student.scatter_(1, i.long(), low)
         for l in (lse, None):
             check(S, student, v, i, T, l, [0, N - 1])
+
+
+@ROWS
+@pytest.mark.parametrize("tail", [1e-3, 1e-5, 1e-6, 3e-7])
+def test_sharp_teachers_and_students_near_them(S, N, V, tail):
+    # r is the small difference of 1 and the record's probabilities
+    K, T = 12, 1.0
+    teacher = logits_of(N, V, "f32", 56, 1.0, 0.0)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    i = torch.rand(N, V, device="cuda", generator=g).topk(K, dim=1).indices
+    rest = torch.logsumexp(teacher.scatter(1, i, -float("inf")).double(), 1)
+    top = torch.randn(N, K, device="cuda", generator=g).double()
+    top += (rest + np.log(1 / tail - 1) - torch.logsumexp(top, 1))[:, None]
+    teacher.scatter_(1, i, top.float())
+    lse = torch.logsumexp(teacher.double(), 1).float()
+    v = teacher.gather(1, i).contiguous()
+    # (a record's probabilities sum to 1 - tail only as far as lse is exact: another lse says another tail)
+    for near in (0.0, 1e-3, 0.1):
+        student = teacher + near * logits_of(N, V, "f32", 57, 1.0, 0.0)
+        check(S, student, v, i.to(torch.int32), T, lse, [0, N // 2, N - 1])
