@@ -424,9 +424,10 @@ __device__ __forceinline__ float shifted(float m, const Pair& x, const Pair& b) 
 // over the cluster, the row's; they become the references (sh.ref, sh.ref_out, sh.ref_in).  0: the row is invalid, 1:
 // it has nothing but -inf outside the record, 2: the rest.  (A function of its own for its registers' sake.)
 template <typename T, int kT>
-__device__ __noinline__ int own_references(const T* row, int V, const Slice<T>& s, const uint32_t* bits,
-                                           const Entry* entries, int n, int rank, int split, Shared& sh) {
+__device__ __noinline__ int own_references(const T* row, int V, const uint32_t* bits, const Entry* entries, int n,
+                                           int rank, int split, Shared& sh) {
   constexpr int kV = Elems<T>::kVec;
+  const Slice<T> s(row, V, rank, split);
   const int tid = threadIdx.x;
   const uint4* r4 = reinterpret_cast<const uint4*>(row + s.head) + s.v0;
   float out = -INFINITY, in = -INFINITY;
@@ -472,8 +473,8 @@ __device__ __noinline__ int own_references(const T* row, int V, const Slice<T>& 
 
 // The row's loss and statistics from its CTAs' parts, by one thread while the others go on to the gradient.  again: of
 // the second pass.
-__device__ __noinline__ void write_loss(const DistillParams& p, int r, const Shared& sh, int split, const Record& rec,
-                                        float c, int flags, int again) {
+__device__ __noinline__ void write_loss(const DistillParams& p, int r, const Shared& sh, int split, Pair inv_t, float c,
+                                        int flags, int again) {
   const Part* parts = sh.parts;
   const float most = sh.most, ref_out = again ? sh.ref_out : most;
   Pair rest{0.f, 0.f}, inside{0.f, 0.f}, mass{0.f, 0.f}, loss{0.f, 0.f};
@@ -484,7 +485,7 @@ __device__ __noinline__ void write_loss(const DistillParams& p, int r, const Sha
     inside = inside + parts[i].top * f;
     if (!(value(parts[i].mass) > 0.f)) continue;  // (its reference may be anything)
     mass = mass + parts[i].mass;
-    loss = loss + (parts[i].against + parts[i].mass * (two_sum(most, -parts[i].ref) * rec.inv_t));
+    loss = loss + (parts[i].against + parts[i].mass * (two_sum(most, -parts[i].ref) * inv_t));
   }
   const bool some_rest = value(rest) > 0.f;
   const float tail = p.teacher_lse ? fmaxf(0.f, value(Pair{1.f, 0.f} - mass)) : 0.f;
@@ -492,12 +493,12 @@ __device__ __noinline__ void write_loss(const DistillParams& p, int r, const Sha
   const Pair ln_rest = some_rest ? log_pair(rest) : Pair{-INFINITY, 0.f};
   loss = loss + mass * ln;
   if (tail > 0.f && some_rest)
-    loss = loss + ((log_pair(Pair{tail, 0.f}) - ln_rest + ln) * tail + two_sum(most, -ref_out) * tail * rec.inv_t);
+    loss = loss + ((log_pair(Pair{tail, 0.f}) - ln_rest + ln) * tail + two_sum(most, -ref_out) * tail * inv_t);
   const bool infinite = (flags & 2) || (tail > 0.f && !some_rest), invalid = flags & 1;
   // (a term past float32's range, of a masked token with p > 0, leaves a pair void: +inf)
   p.loss[r] = invalid ? NAN : infinite || !(fabsf(value(loss)) < INFINITY) ? INFINITY : value(loss);
-  p.stats[2 * r] = invalid ? NAN : shifted(most, rec.inv_t, ln);
-  p.stats[2 * r + 1] = invalid ? NAN : some_rest ? shifted(ref_out, rec.inv_t, ln_rest) : -INFINITY;
+  p.stats[2 * r] = invalid ? NAN : shifted(most, inv_t, ln);
+  p.stats[2 * r + 1] = invalid ? NAN : some_rest ? shifted(ref_out, inv_t, ln_rest) : -INFINITY;
 }
 
 // Loss and statistics of a row, and its gradient (kGrad).  Bound: without the gradient the loads (eight CTAs per SM,
@@ -506,7 +507,7 @@ __device__ __noinline__ void write_loss(const DistillParams& p, int r, const Sha
 // 2304 x 128256 bf16, record of 64, 99 us (6.0 TB/s), 515 x 50001 bf16 20 us; loss and gradient of 2048 x 128256
 // bf16, record of 128, 245 us (4.3 TB/s read and written), 37 x 32001 float32 11 us.
 template <typename T, bool kGrad>
-__global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kernel(DistillParams p) {
+__global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kernel(const __grid_constant__ DistillParams p) {
   extern __shared__ __align__(16) unsigned char raw[];
   Shared& sh = *reinterpret_cast<Shared*>(raw);
   constexpr int kV = Elems<T>::kVec, kT = threads_of(kGrad), kW = kT / 32;
@@ -740,7 +741,7 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
     flags = sh.flags;
     if (!sh.again) break;
     flags &= 1;
-    const int found = own_references<T, kT>(row, p.V, s, bits, entries, n, rank, split, sh);
+    const int found = own_references<T, kT>(row, p.V, bits, entries, n, rank, split, sh);
     if (found == 0) {  // NaN or +inf in the row, or nothing but -inf
       flags |= 1;
       if (tid == 0) sh.k_out = NAN;
@@ -753,7 +754,7 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
   }
 
   const bool invalid = flags & 1;
-  if (rank == 0 && tid == kT - 1) write_loss(p, r, sh, split, rec, c, flags, again);
+  if (rank == 0 && tid == kT - 1) write_loss(p, r, sh, split, rec.inv_t, c, flags, again);
   if (!kGrad) return;
   if (g == 0.f) {
     zero_slice<T, kT>(out, p.V, s, p.vec != 0);
