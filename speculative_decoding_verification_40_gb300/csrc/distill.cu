@@ -226,11 +226,13 @@ __host__ __device__ inline int bitmap_bytes(int per, int kV) { return (per * kV 
 __host__ __device__ inline int entry_bytes(int K) { return (K * static_cast<int>(sizeof(Entry)) + 15) / 16 * 16; }
 
 // Weights 2^(s c + shift), shift the float32 nearest to -ref c: one FFMA and one exponential a logit.  They stand
-// for 2^((s - ref) c) times 1 + miss, the product's own rounding, which is taken out of their sums.
+// for 2^((s - ref) c) times 1 + miss, the product's own rounding, which is taken out of their sums.  A reference of 1e30
+// and more (a mask by the type's lowest value) could leave float32's range with c; logits of that size differ by 2^76 or
+// nothing, so that any power of two in the place of c says the same for every T, without a rounding.
 struct Scale {
   float c, ref, shift, miss;
   __device__ __forceinline__ Scale(float c_, float ref_) {
-    c = c_;
+    c = fabsf(ref_) < 1e30f ? c_ : 0.0009765625f;
     ref = ref_;
     shift = -__fmul_rn(ref, c);
     miss = __fmul_rn(__fmaf_rn(ref, c, shift), kLn2Hi);
@@ -764,7 +766,7 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
   const Scale w(c, ref);
   T* body = out + s.head;
   const bool vec = p.vec != 0;
-  for (int v = tid; v < s.v1 - s.v0; v += kT) grad_vector<T>(kept[v], body, s.v0 + v, vec, c, w.shift, k_out);
+  for (int v = tid; v < s.v1 - s.v0; v += kT) grad_vector<T>(kept[v], body, s.v0 + v, vec, w.c, w.shift, k_out);
   map_ends(row, out, p.V, s, [&](float l) { return w(l) * k_out; });
   if (invalid) return;
   __syncthreads();
@@ -847,7 +849,7 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   while (v < s.v1) {
 #pragma unroll
     for (int u = 0; u < kDU; ++u)
-      if (v + u * kDT < s.v1) grad_vector<T>(q[u], body, v + u * kDT, vec, p.c, w.shift, k_out);
+      if (v + u * kDT < s.v1) grad_vector<T>(q[u], body, v + u * kDT, vec, w.c, w.shift, k_out);
     v += kDU * kDT;
     load();
   }

@@ -23,35 +23,46 @@ HALF = 2.0 ** -24
 MIN = torch.finfo(torch.float32).min
 
 
-def lse64(z):
-    return z.max() + np.log(np.exp(z - z.max()).sum()) if z.size and np.isfinite(z.max()) else -np.inf
+def softmax64(s, T):
+    """(largest, ln of the sum relative to it, softmax) of logits; -inf, -inf and zeros if there is none."""
+    top = s.max() if s.size else -np.inf
+    if not np.isfinite(top):
+        return -np.inf, -np.inf, np.zeros(s.size)
+    e = np.exp((s - top) / T)  # (relative to the largest first: masks of 3e38 leave nothing of the rest in 64 bits)
+    return top, np.log(e.sum()), e / e.sum()
 
 
 def reference(s, values, ids, T, lse):
-    """(loss, [lse, lse outside], gradient, r, the record's probabilities over the vocabulary) of one valid row."""
+    """One valid row: loss, [lse, lse outside], gradient, r, and by token the record's probabilities, q, the shares of
+    the mass outside the record, and -ln of the last two."""
     V = s.size
     on = ids != -1
     i, v = ids[on], values[on]
-    z = s / T
     outside = np.ones(V, bool)
     outside[i] = False
-    total, rest = lse64(z), lse64(z[outside])
-    off = lse64(v / T) if lse is None else lse
-    logp = v / T - off
-    pi = np.exp(logp)
-    r = 0.0 if lse is None else max(0.0, 1.0 - pi.sum())
-    if total - rest > 87 and r <= 2.0 ** -21 * (1 + abs(off)):
+    top, total, q = softmax64(s, T)
+    top_out, rest, share = softmax64(s[outside], T)
+    if lse is None:
+        top_v, off, pi = softmax64(v, T)
+        logp, r = (v - top_v) / T - off, 0.0
+    else:
+        logp = v / T - lse
+        pi = np.exp(logp)
+        r = max(0.0, 1.0 - pi.sum())
+    gap = (top - top_out) / T + total - rest if np.isfinite(top_out) else np.inf
+    if gap > 87 and r <= 2.0 ** -21 * (1 + abs(lse or 0.0)):
         r = 0.0  # the rounding of lse, where the student has nothing beyond the record
     some = pi > 0
-    with np.errstate(divide="ignore"):
-        loss = (pi[some] * (logp[some] - z[i][some] + total)).sum() + (r * (np.log(r) - rest + total) if r > 0 else 0.0)
-    p = np.zeros(V)
+    far = total - (s - top) / T
+    p, out, far_out = np.zeros(V), np.zeros(V), np.zeros(V)
     p[i] = pi
-    grad = (pi.sum() + r) * np.exp(z - total) - p
-    if r > 0 and np.isfinite(rest):
-        with np.errstate(over="ignore"):
-            grad -= np.where(outside, r * np.exp(z - rest), 0.0)
-    return loss, np.array([total, rest]), grad / T, r, p
+    out[outside] = share
+    if np.isfinite(top_out):
+        far_out[outside] = rest - (s[outside] - top_out) / T
+    loss = (pi[some] * (logp[some] + far[i][some])).sum() + (r * (np.log(r) + gap) if r > 0 else 0.0)
+    grad = ((pi.sum() + r) * q - p - r * out) / T
+    stats = np.array([top / T + total, top_out / T + rest if np.isfinite(top_out) else -np.inf])
+    return dict(loss=loss, stats=stats, grad=grad, r=r, p=p, q=q, out=out, far=far, far_out=far_out, gap=gap)
 
 
 def check(S, student, v, i, T, lse, rows=None, stats=None):
@@ -63,38 +74,32 @@ def check(S, student, v, i, T, lse, rows=None, stats=None):
     eps = torch.finfo(student.dtype).eps
     T = float(np.float32(T))
     a = (V / 256 + 84) * HALF
-    for r in range(N) if rows is None else sorted(set(rows)):
-        s64, i64 = F.rows64(student[r]), i[r].cpu().numpy()
-        off = None if lse is None else float(lse[r])
-        L, want, G, tail, p = reference(s64, F.rows64(v[r]), i64, T, off)
-        z = s64 / T
-        outside = np.ones(V, bool)
-        outside[i64[i64 >= 0]] = False
+    most = float(np.finfo(np.float32).max)  # beyond it a float32 is infinite
+    for n in range(N) if rows is None else sorted(set(rows)):
+        off = None if lse is None else float(lse[n])
+        w = reference(F.rows64(student[n]), F.rows64(v[n]), i[n].cpu().numpy(), T, off)
+        L, G, r, p, far = w["loss"], w["grad"], w["r"], w["p"], w["far"]
+        gap, log_r, r_off = 0.0, 0.0, 0.0
+        if r > 0:
+            gap, log_r = w["gap"], abs(np.log(r))
+            r_off = 2 * HALF * r + 2.0 ** -37 * (1 + abs(off) / 8)
         some = p > 0
-        size = np.abs(off) if off is not None else 0.0
-        r_off = 2 * HALF * tail + 2.0 ** -38 * (1 + size / 8) * 2 if tail > 0 else 0.0
-        gap = want[0] - want[1] if tail > 0 else 0.0
-        log_r = np.abs(np.log(tail)) if tail > 0 else 0.0
-        terms = p[some] * (np.abs(np.log(p[some])) + np.abs(z[some] - want[0]))
-        tl = 3 * a + 8 * HALF * terms.sum() + tail * 2 * a + r_off * (log_r + gap + 2) + 8 * HALF * tail * (log_r + gap)
-        most = float(np.finfo(np.float32).max)  # beyond it a float32 is infinite
-        for x in (loss[r].item(), loss2[r].item()):
-            assert x == L or (L > most * (1 - HALF) and x == np.inf) or abs(x - L) <= tl + HALF * min(L, most), (r, x, L, tl)
-        got = st[r].tolist()
-        for x, y in zip(got, want):
-            assert x == y or (y < -most and x == -np.inf) or abs(x - y) <= a + HALF * abs(y), (r, got, want)
-        rel = lambda x: 2 * a + 6 * HALF * x + 2.0 ** -20  # noqa: E731
-        x_in, x_out = np.abs(np.where(np.isfinite(z), z - want[0], 0)), np.abs(np.where(np.isfinite(z), z - want[1], 0))
-        x_out = np.where(np.isfinite(x_out), x_out, 0.0)
-        out = np.where(outside & np.isfinite(z), np.exp(np.minimum(z - want[1], 1)), 0.0) if tail > 0 else np.zeros(V)
-        q = np.exp(z - want[0])
+        terms = (p[some] * (np.abs(np.log(p[some])) + np.abs(far[some]))).sum()
+        tl = 3 * a + 8 * HALF * terms + r * 2 * a + r_off * (log_r + gap + 2) + 8 * HALF * r * (log_r + gap)
+        for x in (loss[n].item(), loss2[n].item()):
+            assert x == L or (L > most * (1 - HALF) and x == np.inf) or abs(x - L) <= tl + HALF * min(L, most), (n, x, L, tl)
+        got = st[n].tolist()
+        for x, y in zip(got, w["stats"]):
+            assert x == y or (y < -most and x == -np.inf) or abs(x - y) <= a + HALF * abs(y), (n, got, w["stats"])
+        rel = lambda x: 2 * a + 6 * HALF * np.where(np.isfinite(x), np.abs(x), 0.0) + 2.0 ** -20  # noqa: E731
         for k, x in enumerate((grad, grad2)):
-            held = 2 * HALF * np.abs(want[0 if tail == 0 or np.isinf(want[1]) else [0, 1]]).sum() if k == 0 else 0.0
-            tg = (q * (p.sum() + tail) * (rel(x_in) + held) + out * (tail * (rel(x_out) + held) + r_off) + 2 * HALF * p +
-                  2.0 ** -60 * (p.sum() + tail)) / T + eps / 2 * np.abs(G) + 2.0 ** -126
-            d = np.abs(F.rows64(x[r]) - G) - tg * 1.01
+            held = 2 * HALF * np.abs(w["stats"][0 if r == 0 or np.isinf(gap) else [0, 1]]).sum() if k == 0 else 0.0
+            tg = (w["q"] * (p.sum() + r) * (rel(far) + held) + w["out"] * (r * (rel(w["far_out"]) + held) + r_off) +
+                  2 * HALF * p + 2.0 ** -60 * (p.sum() + r)) / T + eps / 2 * np.abs(G) + 2.0 ** -126
+            y = F.rows64(x[n])
+            d = np.abs(y - G) - tg * 1.01
             at = int(np.argmax(np.where(np.isnan(d), np.inf, d)))
-            assert d[at] <= 0, (r, k, at, F.rows64(x[r])[at], G[at], tg[at], outside[at])
+            assert d[at] <= 0, (n, k, at, y[at], G[at], tg[at])
     return loss, grad, loss2, grad2
 
 
@@ -159,6 +164,33 @@ def test_student_all_but_certain_of_the_record(S, N, V, T, dtype):
             stats = torch.stack([torch.logsumexp(z, 1), torch.logsumexp(out, 1)], 1).float()
             pick = [t[rows].contiguous() for t in (x, v, i, lse)]
             check(S, pick[0], pick[1], pick[2], T, pick[3], None, stats)
+
+
+@ROWS
+@pytest.mark.parametrize("T", [0.7, 1.0, 8.0, 2.0 ** 40])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_student_masked_by_its_types_lowest_value(S, N, V, T, dtype):
+    # everywhere but at the record's tokens, which lie in the first half of the row
+    student, v, i, lse = batch(N, V // 2, 20, dtype, T, 62)
+    low = torch.finfo(student.dtype).min
+    x = torch.full((N, V), low, device="cuda", dtype=student.dtype)
+    x.scatter_(1, i.long(), student.gather(1, i.long()))
+    # (with a tail, the masked tokens' gradients take 1 / T times their number from a statistic of 3e38)
+    out = check(S, x, v, i, T, None, [0, N // 2, N - 1])
+    for l, g in ((None, out[1]), (None, out[3])):
+        assert torch.isfinite(g).all()
+    loss, stats = S.distill_forward(x, v, i, T, teacher_lse=lse)
+    for g in (S.distill_backward(x, v, i, T, stats, teacher_lse=lse), S.distill_loss_grad(x, v, i, T, teacher_lse=lse)[1]):
+        assert torch.isfinite(g).all() and not torch.isnan(loss).any()
+        assert (g.gather(1, i.long()).float().sum(1).abs() < 2).all()
+    x.fill_(low)  # all of them alike
+    if T >= 1:
+        check(S, x, v, i, T, None, [0, N - 1])
+    else:  # 3.4e38 / 0.7 is no float32: the statistics are infinite, and the backward pass has nothing to go by
+        loss, stats = S.distill_forward(x, v, i, T)
+        assert torch.isfinite(loss).all() and (stats == -float("inf")).all()
+        assert torch.isnan(S.distill_backward(x, v, i, T, stats)).all()
+        assert torch.isfinite(S.distill_loss_grad(x, v, i, T)[1]).all()
 
 
 @ROWS
