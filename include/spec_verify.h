@@ -341,7 +341,10 @@ int spec_top_logits(const void* logits, int dtype, float temperature, int R, int
  * with its target is what raises the acceptance rate that spec_accept_stats measures.
  *  - teacher_lse [N] (the teacher's log-sum-exp at this T): p_i = exp(values_i / T - lse), and the mass
  *    beyond the record, r = max(0, 1 - sum p_i), is one more outcome, compared with the student's mass
- *    outside the record: loss = sum_i p_i ln(p_i / q_i) + r ln(r / Q_rest).
+ *    outside the record: loss = sum_i p_i ln(p_i / q_i) + r ln(r / Q_rest).  An r of at most
+ *    2^-21 (1 + |lse|), which the rounding of lse leaves where the record holds all that the teacher gives
+ *    mass to (a constrained vocabulary, K = V), counts as 0 where the student too has less than e^-87 of
+ *    its mass beyond the record.
  *  - teacher_lse NULL: p is the softmax of the record's values / T, and loss = sum_i p_i ln(p_i / q_i).
  * A term with p_i = 0 (or r = 0) is 0; a token with p_i > 0 whose student logit
  * is -inf makes the loss +inf.  Sums are float32, compensated; those over the

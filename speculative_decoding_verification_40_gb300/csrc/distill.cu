@@ -97,6 +97,14 @@ __device__ __forceinline__ Pair probability(const Pair& x) {
   return Pair{e.hi * scale, e.lo * scale};
 }
 
+// The teacher's mass beyond the record, given the record's, its log-sum-exp and how far the student's own mass there lies
+// below its whole (in the logarithm): what the rounding of a float32 log-sum-exp leaves (eight steps of 2^-24 of
+// 1 + |lse|: its own, its logits', and those of a float32 sum) is none where the student has next to nothing there.
+__device__ __forceinline__ float beyond(const Pair& mass, float lse, float gap) {
+  const float tail = fmaxf(0.f, value(Pair{1.f, 0.f} - mass));
+  return gap > 87.f && tail <= __fmul_rn(4.76837158e-7f, 1.f + fabsf(lse)) ? 0.f : tail;
+}
+
 template <int kT>
 __device__ __forceinline__ Pair block_sum(Pair v, Pair* part) {
   v = warp_sum(v);
@@ -490,9 +498,10 @@ __device__ __noinline__ void write_loss(const DistillParams& p, int r, const Sha
     loss = loss + (parts[i].against + parts[i].mass * (two_sum(most, -parts[i].ref) * inv_t));
   }
   const bool some_rest = value(rest) > 0.f;
-  const float tail = p.teacher_lse ? fmaxf(0.f, value(Pair{1.f, 0.f} - mass)) : 0.f;
   const Pair ln = log_pair(again ? rest * step(ref_out, most, c) + inside * step(sh.ref_in, most, c) : rest + inside);
   const Pair ln_rest = some_rest ? log_pair(rest) : Pair{-INFINITY, 0.f};
+  const float gap = ln.hi - ln_rest.hi + (most - ref_out) * inv_t.hi;
+  const float tail = p.teacher_lse ? beyond(mass, p.teacher_lse[r], gap) : 0.f;
   loss = loss + mass * ln;
   if (tail > 0.f && some_rest)
     loss = loss + ((log_pair(Pair{tail, 0.f}) - ln_rest + ln) * tail + two_sum(most, -ref_out) * tail * inv_t);
@@ -723,7 +732,8 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
         }
         // a token of the record has q = weight f_in / total, f_in the step from its reference to the common one; any
         // other weighs f_out / total in the row and f / rest in the tail
-        const float tail = p.teacher_lse ? fmaxf(0.f, value(Pair{1.f, 0.f} - mass)) : 0.f, both = value(mass) + tail;
+        const float gap = again ? (most - sh.ref_out) * p.inv_t - logf(__fdividef(rest, total)) : 0.f;
+        const float tail = p.teacher_lse ? beyond(mass, p.teacher_lse[r], gap) : 0.f, both = value(mass) + tail;
         // (approximate quotients, two steps of 2^-23: their operands' weights carry the exponential's 2^-22 each)
         const float scale = __fmul_rn(g, p.inv_t), f = again ? 1.f : f_out;
         const float share = tail > 0.f && rest > 0.f ? __fdividef(__fmul_rn(tail, f), rest) : 0.f;
@@ -824,7 +834,8 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   mass = block_sum<kDT>(mass, part);
   bad |= !(fabsf(lse) < INFINITY);  // the forward pass found the row invalid
   bad = __syncthreads_or(bad);
-  const float tail = p.teacher_lse ? fmaxf(0.f, value(Pair{1.f, 0.f} - mass)) : 0.f;
+  const float gap = lse - lse_rest;
+  const float tail = p.teacher_lse ? beyond(mass, teacher_lse, gap) : 0.f;
   const float both = value(mass + Pair{tail, 0.f}), scale = __fmul_rn(g, rec.inv_t.hi);
   // weights 2^(s c + shift), shift the float32 nearest to -T lse c; what the roundings of it and of T lse miss goes
   // into the factors
@@ -836,7 +847,6 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   };
   // tokens outside the record: q less their share of the tail, relative to lse, or to lse_rest where that is so far
   // below that q is nothing and the quotient of the two would leave float32's range
-  const float gap = lse - lse_rest;
   const bool apart = gap > 40.f && gap < INFINITY;
   const float ratio = exp_pair(two_sum(apart ? lse_rest : lse, apart ? -lse : -lse_rest));
   const float share = tail > 0.f && lse_rest > -INFINITY ? tail * (apart ? 1.f : ratio) : 0.f;

@@ -220,3 +220,35 @@ def test_sharp_teachers_and_students_near_them(S, N, V, tail):
     for near in (0.0, 1e-3, 0.1):
         student = teacher + near * logits_of(N, V, "f32", 57, 1.0, 0.0)
         check(S, student, v, i.to(torch.int32), T, lse, [0, N // 2, N - 1])
+
+
+@ROWS
+@pytest.mark.parametrize("T", [0.7, 1.0])
+@pytest.mark.parametrize("mask", [-float("inf"), MIN, -1e5])
+def test_records_that_hold_every_token_of_weight(S, N, V, T, mask):
+    # both models masked alike: at most K tokens are allowed
+    K, allowed = 64, 40
+    g = torch.Generator(device="cuda").manual_seed(2)
+    i = torch.rand(N, V, device="cuda", generator=g).topk(K, dim=1).indices
+    teacher = torch.full((N, V), mask, device="cuda")
+    student = torch.full((N, V), mask, device="cuda")
+    teacher.scatter_(1, i[:, :allowed], 3 * torch.randn(N, allowed, device="cuda", generator=g) + 10)
+    student.scatter_(1, i[:, :allowed], 3 * torch.randn(N, allowed, device="cuda", generator=g))
+    values, ids, lse = S.top_logits(teacher, K, T)
+    for l in (lse, None):
+        for made in (values, values.masked_fill(ids < 0, float("nan"))):
+            out = check(S, student, made, ids, T, l, [0, N // 2, N - 1])
+            assert all(torch.isfinite(t).all() for t in out) and out[0].abs().max() < 100
+    # a teacher that gives real weight to what its student excludes: +inf where it is -inf
+    other = (lse.double() + 0.01).float()
+    loss = S.distill_forward(student, values, ids, T, teacher_lse=other)[0]
+    assert (loss > 1).all() and (mask > -float("inf") or torch.isinf(loss).all())
+
+
+@pytest.mark.parametrize("V", [1, 7, 300, 1000])
+def test_records_of_the_whole_vocabulary(S, V):
+    N = 64
+    teacher, student = logits_of(N, V, "f32", 58), logits_of(N, V, "f32", 59)
+    values, ids, lse = S.top_logits(teacher, V)
+    out = check(S, student, values, ids, 1.0, lse)
+    assert all(torch.isfinite(t).all() for t in out)
