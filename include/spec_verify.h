@@ -307,10 +307,12 @@ int spec_sample_rows_masked(const void* logits, int dtype, const float* uniforms
  *   workspace    >= 256 bytes, 256-byte aligned: only the error word is used, so any workspace will do, and
  *                calls that overlap on the GPU may share it
  *
- * Cuts and draws are decided by sums exact to ten digits, whatever their order:
- * the same call gives the same tokens every time, those of the definition
- * above (a weight below 2^-46 of the largest adds nothing to them, but at a
- * uniform of 0 the first token of any weight is drawn).  A row is invalid if it
+ * Cuts and draws are decided by sums of weights rounded to 2^-45 of the largest
+ * (and exact to 2^-34 of themselves), whatever their order and the path a row
+ * takes: the same call gives the same tokens every time, those of the definition
+ * above but for a border within some 1e-9 of the total, V 2^-46 at most (a weight
+ * below 2^-46 adds nothing, but at a uniform of 0 the first token of any weight is
+ * drawn).  A row is invalid if it
  * holds NaN or +inf or only -inf, or if its uniform or one of its parameters lies
  * outside its range; what the device finds is recorded in the error word.  A
  * scalar outside its range returns SPEC_ERR_ARG. */

@@ -18,6 +18,7 @@
 // holds) is decided by exact selection over the whole row by the first CTA.
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "../../include/spec_verify.h"
 #include "common.cuh"
@@ -56,7 +57,26 @@ struct CutResult {
 };
 
 struct Words {
-  unsigned int lo[kBins], mid[kBins], hi[kBins];
+  unsigned int lo[kBins], mid[kBins], hi[kBins], top[kBins];
+};
+
+// A histogram as Hist (select.cuh) of masses up to 2^45, bits 42 up of every value in a fourth word: with three, 2^18 of
+// the largest weight in one bin would wrap the third.
+struct WideHist : Hist {
+  unsigned int* top;
+  __device__ __forceinline__ unsigned long long get(int b) const {
+    return (static_cast<unsigned long long>(top[b]) << 42) + Hist::get(b);
+  }
+  __device__ __forceinline__ void add(int b, unsigned long long v) const {
+    Hist::add(b, v & ((1ull << 42) - 1));
+    const unsigned int t = static_cast<unsigned int>(v >> 42);
+    if (t) atomicAdd(top + b, t);
+  }
+  template <int kThreads>
+  __device__ __forceinline__ void zero(int nb) const {
+    for (int k = threadIdx.x; k < nb; k += kThreads) top[k] = 0u;
+    Hist::zero<kThreads>(nb);
+  }
 };
 
 static_assert(kFW * kGroup * sizeof(float) <= kListCap * sizeof(unsigned long long), "the second pass gathers there");
@@ -233,8 +253,14 @@ __device__ CutResult select_key(const S& src, uint32_t lo, uint32_t hi, unsigned
                                 Shared& sh) {
   const int tid = threadIdx.x;
   constexpr bool kRow = kNB == kBins;
-  const Hist h{kRow ? sh.row_hist.lo : sh.hist.lo, !kMass ? nullptr : kRow ? sh.row_hist.mid : sh.hist.mid,
-               !kMass ? nullptr : kRow ? sh.row_hist.hi : sh.hist.hi};
+  const Hist narrow{kRow ? sh.row_hist.lo : sh.hist.lo, !kMass ? nullptr : kRow ? sh.row_hist.mid : sh.hist.mid,
+                    !kMass ? nullptr : kRow ? sh.row_hist.hi : sh.hist.hi};
+  using H = std::conditional_t<kRow && kMass, WideHist, Hist>;
+  H h;
+  if constexpr (kRow && kMass)
+    h = H{narrow, sh.row_hist.top};
+  else
+    h = narrow;
   unsigned long long above = 0;
   constexpr int kDigit = kNB == 2048 ? 11 : 9;
   static_assert(kNB == 1 << kDigit, "a digit fills the bins");
@@ -1234,8 +1260,7 @@ __device__ __noinline__ void sample_from_row(const T* row, int V, const Weight& 
   const float M = weight.M;
   const uint32_t hi = fkey(M);
   uint32_t tau = kKeyNegInf + 1;
-  // nucleus masses in 2^-41 (rounded): the histogram's words hold any sum of them
-  auto units = [&](float l, int) { return (weight(l) + 8ull) >> 4; };
+  auto units = [&](float l, int) { return weight(l); };
   if (f.t == 0.f) {
     tau = hi;
   } else {

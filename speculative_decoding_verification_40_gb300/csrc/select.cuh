@@ -75,8 +75,8 @@ struct Hist {
 
 // Over the nb bins of h read from the highest bin down: the bin where the running sum first reaches
 // need (1 <= need <= total), the sum above that bin, and the total.  Every thread gets the result.
-template <int kThreads>
-__device__ Pick pick_from_top(const Hist& h, int nb, unsigned long long need, unsigned long long* wsum, Pick* out) {
+template <int kThreads, typename H>
+__device__ Pick pick_from_top(const H& h, int nb, unsigned long long need, unsigned long long* wsum, Pick* out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = nb / kThreads;  // bins per thread, thread 0 holding the highest
   unsigned long long local = 0;

@@ -1,0 +1,47 @@
+"""Filtered sampling next to its borders (GPU, against 64 bits): nuclei whose end is decided by the row's tail alone,
+whatever path a row takes."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_filtered import S, check  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+V = 262144
+
+
+def near_one(base, extra, lo, hi, n=6):
+    """n pairs (b, p) of float32 with p (base + e^b + extra) - 1 between lo and hi and e^b about a third."""
+    found = []
+    b = np.float32(-np.log(3.0))
+    while len(found) < n:
+        b = np.nextafter(b, np.float32(0))
+        total = base + np.exp(np.float64(b)) + extra
+        p = np.float32(1 / total)
+        for q in (np.nextafter(p, np.float32(0)), p, np.nextafter(p, np.float32(1))):
+            if lo < np.float64(q) * total - 1 < hi:
+                found.append((b, q))
+    return found
+
+
+@pytest.mark.parametrize("copies", [1, 20, 90])  # eight to one CTA per row
+@pytest.mark.parametrize("u", [0.0, 0.9])
+def test_a_flat_tail_of_small_weights_counts(S, copies, u):
+    # 262142 tokens of five units of 2^-45 each, all alike, so that no list holds them: 3.7e-8 in all
+    d = np.float32(np.log(5 * 2.0 ** -45))
+    tail = (V - 2) * np.exp(np.float64(d))
+    pairs = near_one(1.0, tail, 4e-9, 2e-8)  # with the tail the nucleus passes the first token, without it it does not
+    x = torch.full((len(pairs), V), float(d))
+    for r, (b, _) in enumerate(pairs):
+        x[r, 600], x[r, 700] = 0.0, float(b)
+    R = len(pairs) * copies
+    logits = x.cuda().repeat(copies, 1)
+    p = np.tile([q for _, q in pairs], copies)
+    uu = torch.full((R,), u, device="cuda")
+    n = len(pairs)
+    f = lambda a: torch.tensor(np.asarray(a), dtype=torch.float32, device="cuda")  # noqa: E731
+    got = S.sample_filtered(logits, uu, 1.0, 0, f(p), 0.0)
+    check(S, logits[-n:], uu[-n:], np.ones(n), np.zeros(n, int), p[-n:], np.zeros(n), [t[-n:] for t in got], 0)
+    assert all(torch.equal(t, t[-n:].repeat(copies)) for t in got)
