@@ -567,7 +567,7 @@ __device__ __noinline__ unsigned int sum_groups(const T* row, int V, int g0, int
 // them, 32 at a time: a weight is 45 instructions, which one lane in 32 would otherwise make the others wait for.
 template <typename T>
 __device__ __noinline__ unsigned long long bracket_groups(const T* row, int V, int g0, int g1, float lo, float hi,
-                                                          Weight weight, float u, Shared& sh, uint32_t sums) {
+                                                          Weight weight, Shared& sh, uint32_t sums) {
   const int lane = threadIdx.x & 31;
   float* gathered = reinterpret_cast<float*>(sh.w) + (threadIdx.x >> 5) * kGroup;
   const unsigned int before = (1u << lane) - 1u;
@@ -635,7 +635,7 @@ __device__ __noinline__ unsigned long long bracket_groups(const T* row, int V, i
                if (kept > 0) {
                  __syncwarp();
 #pragma unroll 1
-                 for (int i = lane; i < kept; i += 32) sum += draw_unit(weight(gathered[i]), gathered[i], weight, u);
+                 for (int i = lane; i < kept; i += 32) sum += weight(gathered[i]);  // (all of them count: a nucleus's)
                  __syncwarp();
                  sum = warp_sum_u64(sum);
                  kept = 0;
@@ -1309,9 +1309,9 @@ __device__ bool second_pass(const T* row, int V, const Slice& s, uint32_t key_lo
   unsigned long long rest = 0;
   unsigned int least = 0xffffffffu;
   if (nucleus)
-    rest = bracket_groups(row, V, g0, g1, key_float(key_lo), key_float(key_hi), weight, f.u, sh, to);
+    rest = bracket_groups(row, V, g0, g1, key_float(key_lo), key_float(key_hi), weight, sh, to);
   else
-    least = sum_groups(row, V, g0, g1, key_hi, weight, f.u, to);
+    least = sum_groups(row, V, g0, g1, key_hi, weight, sums ? 1.f : f.u, to);  // (a total has no units for u = 0)
   if (!join(s, sh, rest, 0.f, least)) return !sums;
   if (sums) return true;
   uint32_t lowest = sh.lowest[0], tau = key_hi;

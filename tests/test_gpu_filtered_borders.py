@@ -45,3 +45,24 @@ def test_a_flat_tail_of_small_weights_counts(S, copies, u):
     got = S.sample_filtered(logits, uu, 1.0, 0, f(p), 0.0)
     check(S, logits[-n:], uu[-n:], np.ones(n), np.zeros(n, int), p[-n:], np.zeros(n), [t[-n:] for t in got], 0)
     assert all(torch.equal(t, t[-n:].repeat(copies)) for t in got)
+
+
+@pytest.mark.parametrize("copies", [1, 20, 90])
+@pytest.mark.parametrize("u", [0.0, 0.9])
+def test_weights_below_the_smallest_unit_do_not_count(S, copies, u):
+    # 3000 tokens that the list sees a part of, the rest 40 below the largest: the exact total decides the first cut
+    x = torch.full((1, V), -40.0)
+    at = torch.arange(3000) * 87 + 3
+    x[0, at] = torch.linspace(-14.0, -9.0, 3000)
+    base = 1.0 + np.exp(x[0, at].double().numpy()).sum()
+    pairs = near_one(base, 0.0, -5e-9, -2e-9)  # the first token alone is the nucleus
+    x = x.repeat(len(pairs), 1)
+    for r, (b, _) in enumerate(pairs):
+        x[r, 600], x[r, 500] = 0.0, float(b)
+    logits = x.cuda().repeat(copies, 1)
+    n = len(pairs)
+    p = np.tile([q for _, q in pairs], copies)
+    uu = torch.full((n * copies,), u, device="cuda")
+    got = S.sample_filtered(logits, uu, 1.0, 0, torch.tensor(p, device="cuda"), 0.0)
+    tokens = check(S, logits[-n:], uu[-n:], np.ones(n), np.zeros(n, int), p[-n:], np.zeros(n), [t[-n:] for t in got], 0)
+    assert (tokens == 600).all() and all(torch.equal(t, t[-n:].repeat(copies)) for t in got)
