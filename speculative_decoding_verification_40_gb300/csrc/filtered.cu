@@ -37,7 +37,9 @@ constexpr int kGroup = 512;         // tokens per group of the draw
 constexpr int kGroups = kMaxVocab / kGroup;
 static_assert(kGroup == 2 * kFT && kGroups == 2 * kFT, "the draw's scans take two values per thread");
 constexpr int kMaxSplit = 8;        // CTAs per row (the portable cluster size)
+constexpr int kLeastSlice = 2048;   // logits that a CTA of several takes at least
 constexpr int kListCap = 2400;      // logits a row's list holds
+static_assert(kListCap < 2 * kLeastSlice, "a row that its list holds is one CTA's: a cluster's CTAs meet in estimate()");
 constexpr int kListAim = 1000;      // logits the estimate aims at; vocabularies sorted by frequency give half to twice
 constexpr int kSample = 1024;       // sampled maxima behind the estimate
 constexpr int kSampleBins = 512;    // and the bins that rank them
@@ -999,7 +1001,6 @@ __device__ bool stream_cluster(const T* row, int V, const Slice& s, Stream<T>& q
   const float below = sum ? stream<T, true>(row, V, s, q, aim, c, sh, floor_of, &rest)
                           : stream<T, false>(row, V, s, q, aim, c, sh, floor_of, &rest);
   if (threadIdx.x == 0) sh.below = below;
-  if (s.split > 1 && V <= kListCap) cluster_wait_acquire();  // (longer rows: estimate() has waited)
   return join(s, sh, rest, 0.f, 0xffffffffu);
 }
 
@@ -1760,10 +1761,10 @@ __global__ void __launch_bounds__(kFT, 4) top_logits_kernel(TopParams q) {
 
 }  // namespace
 
-// CTAs per row: doubled while the batch gives at most `most` CTAs and a CTA is left 2048 logits.
+// CTAs per row: doubled while the batch gives at most `most` CTAs and a CTA is left kLeastSlice logits.
 static int row_split(int R, int V, int most) {
   int split = 1;
-  while (split < kMaxSplit && 2LL * R * split <= most && V / (2 * split) >= 2048) split *= 2;
+  while (split < kMaxSplit && 2LL * R * split <= most && V / (2 * split) >= kLeastSlice) split *= 2;
   return split;
 }
 
