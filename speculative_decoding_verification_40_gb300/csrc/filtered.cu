@@ -43,6 +43,7 @@ static_assert(kListCap < 2 * kLeastSlice, "a row that its list holds is one CTA'
 constexpr int kListAim = 1000;      // logits the estimate aims at; vocabularies sorted by frequency give half to twice
 constexpr int kSample = 1024;       // sampled maxima behind the estimate
 constexpr int kSampleBins = 512;    // and the bins that rank them
+constexpr int kBinMaxima = 48;      // maxima in the bin of the wanted rank that are ranked no further
 constexpr int kListBins = 512;      // bins of a histogram over the list
 constexpr int kBracketAim = 1100;   // logits the second pass's list aims at
 constexpr int kProbe = 16;          // vectors per thread of the sample that places it
@@ -688,6 +689,46 @@ __device__ __forceinline__ Slice slice_of(const T* row, int V, int rank, int spl
 constexpr int kU = 4;  // vectors in flight per thread
 constexpr int kAhead = 128;  // vectors per run that the L2 gets ahead of the stream
 
+// The bins per logit of a histogram of maxima between lo and hi.  (Maxima more than 1e30 below hi, masked by their type's
+// lowest value, share the last bin; 0: they are one value.)
+__device__ __forceinline__ float sample_scale(float hi, float lo) {
+  const float range = fminf(hi - lo, 1e30f);
+  return range > 0.f ? __fdividef(static_cast<float>(kSampleBins) - 0.5f, range) : 0.f;
+}
+
+__device__ __forceinline__ int sample_bin(uint32_t key, float hi, float scale) {
+  return min(kSampleBins - 1, static_cast<int>((hi - key_float(key)) * scale));
+}
+
+struct SampleRank {
+  int bin, above, in;  // the bin the want-th maximum from the top is in (-1: there are fewer), those above it, in it
+};
+
+// Every warp by itself, over sh.sample.count: lane i holds 16 bins.
+__device__ __forceinline__ SampleRank sample_rank(const Shared& sh, int want) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kPer = kSampleBins / 32;
+  int mine = 0;
+#pragma unroll 4
+  for (int j = 0; j < kPer; ++j) mine += sh.sample.count[lane * kPer + j];
+  int incl = mine;
+#pragma unroll 1
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  const unsigned int reached = __ballot_sync(0xffffffffu, incl >= want);
+  if (reached == 0) return SampleRank{-1, 0, 0};
+  const int who = __ffs(reached) - 1;
+  int run = __shfl_sync(0xffffffffu, incl - mine, who), bin = who * kPer;
+#pragma unroll 1
+  for (;; ++bin) {
+    const int in = sh.sample.count[bin];
+    if (run + in >= want) return SampleRank{bin, run, in};
+    run += in;
+  }
+}
+
 // The value some `aim` logits of the row lie at or above.  Every thread knows four maxima of the `sampled` logits
 // each that it loaded first, at 32 places of the CTA's slice; an aim of a share a of the row's logits corresponds
 // to the share 1 - exp(-a sampled) of those maxima, and the value of that rank among 1024 of them, the same
@@ -718,6 +759,8 @@ __device__ float estimate(const Slice& s, int V, int aim, const float (&top)[4],
     key[1] = all.y;
     key[2] = all.z;
     key[3] = all.w;
+  } else {
+    sh.sample.key[tid] = make_uint4(key[0], key[1], key[2], key[3]);
   }
   uint32_t lo_key = 0xffffffffu, hi_key = 0u;
 #pragma unroll
@@ -725,45 +768,72 @@ __device__ float estimate(const Slice& s, int V, int aim, const float (&top)[4],
     lo_key = min(lo_key, key[u] > kKeyNegInf ? key[u] : 0xffffffffu);
     hi_key = max(hi_key, key[u]);
   }
-  lo_key = __reduce_min_sync(0xffffffffu, lo_key);
-  hi_key = __reduce_max_sync(0xffffffffu, hi_key);
-  if (lane == 0) sh.wsum[warp] = (static_cast<unsigned long long>(hi_key) << 32) | lo_key;
-  sh.sample.count[tid] = 0u;
-  sh.sample.count[tid + kFT] = 0u;
-  __syncthreads();
-  const unsigned long long both = sh.wsum[lane % kFW];
-  lo_key = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(both));
-  hi_key = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(both >> 32));
+  // over the block, with the bins cleared
+  auto extremes = [&](uint32_t& low, uint32_t& high) {
+    sh.sample.count[tid] = 0u;
+    sh.sample.count[tid + kFT] = 0u;
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    if (lane == 0) sh.wsum[warp] = (static_cast<unsigned long long>(high) << 32) | low;
+    __syncthreads();
+    const unsigned long long both = sh.wsum[lane % kFW];
+    low = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(both));
+    high = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(both >> 32));
+  };
+  extremes(lo_key, hi_key);
   if (hi_key <= kKeyNegInf || !(key_float(hi_key) < INFINITY)) return -INFINITY;  // nothing finite, or +inf
-  const float hi = key_float(hi_key), range = hi - key_float(lo_key);
-  const float bins = range > 0.f ? __fdividef(static_cast<float>(kSampleBins) - 0.5f, range) : 0.f;
+  const float share = __fdividef(static_cast<float>(aim), static_cast<float>(V)), most = key_float(hi_key);
+  int want =
+      max(1, min(kSample, __float2int_rn(kSample * (1.f - fast_exp2(-1.442695f * share * sampled)))));
+  float hi = most, scale = sample_scale(hi, key_float(lo_key));
 #pragma unroll
   for (int u = 0; u < 4; ++u)
-    if (key[u] > kKeyNegInf)
-      atomicAdd(&sh.sample.count[min(kSampleBins - 1, static_cast<int>((hi - key_float(key[u])) * bins))], 1u);
+    if (key[u] > kKeyNegInf) atomicAdd(&sh.sample.count[sample_bin(key[u], hi, scale)], 1u);
   __syncthreads();
-  const float share = __fdividef(static_cast<float>(aim), static_cast<float>(V));
-  const int want =
-      max(1, min(kSample, __float2int_rn(kSample * (1.f - fast_exp2(-1.442695f * share * sampled)))));
-  // every warp by itself: lane i holds 16 bins; the bin the want-th maximum is in
-  constexpr int kPer = kSampleBins / 32;
-  int mine = 0;
-#pragma unroll 4
-  for (int j = 0; j < kPer; ++j) mine += sh.sample.count[lane * kPer + j];
-  int incl = mine;
+  SampleRank rank = sample_rank(sh, want);
+  if (rank.bin < 0) return -INFINITY;  // fewer finite maxima than that
+  // Where the bin of the wanted rank holds many maxima (a stretch of logits masked by a finite value, -1e4 or the type's
+  // lowest, makes the bins as wide as its distance), once more with bins between the smallest and the largest maximum of
+  // that bin; a single value, the mask itself, is left out where others lie above it (a list cannot hold its ties).
+  // 512 rows of 152064, a third of them masked by -1e4, top 64: 90 us (741 where the list ran over and one CTA selected
+  // from the row).
+  if (__builtin_expect(rank.in > kBinMaxima && scale > 0.f, 0)) {
+    int others = 0;
 #pragma unroll 1
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += y;
+    for (int round = 0; rank.in > kBinMaxima && round < 4; ++round) {
+      const uint4 all = sh.sample.key[tid];
+      want -= rank.above;
+      others |= rank.above;
+      uint32_t low = 0xffffffffu, high = 0u;
+      auto narrow = [&](uint32_t k) {
+        if (k < lo_key || k > hi_key || sample_bin(k, hi, scale) != rank.bin) return;
+        low = min(low, k);
+        high = max(high, k);
+      };
+      narrow(all.x);
+      narrow(all.y);
+      narrow(all.z);
+      narrow(all.w);
+      __syncthreads();  // the bins have been read
+      extremes(low, high);
+      lo_key = low;
+      hi_key = high;
+      hi = key_float(hi_key);
+      scale = sample_scale(hi, key_float(lo_key));
+      if (scale == 0.f) return floor_of(others ? key_float(lo_key + 1) : hi, most);
+      auto count = [&](uint32_t k) {
+        if (k >= lo_key && k <= hi_key) atomicAdd(&sh.sample.count[sample_bin(k, hi, scale)], 1u);
+      };
+      count(all.x);
+      count(all.y);
+      count(all.z);
+      count(all.w);
+      __syncthreads();
+      rank = sample_rank(sh, want);
+    }
   }
-  const unsigned int reached = __ballot_sync(0xffffffffu, incl >= want);
-  if (reached == 0) return -INFINITY;  // fewer finite maxima than that
-  const int who = __ffs(reached) - 1;
-  int run = __shfl_sync(0xffffffffu, incl - mine, who), bin = who * kPer;
-#pragma unroll 1
-  for (; run < want; ++bin) run += sh.sample.count[bin];
-  const float value = bins > 0.f ? hi - __fdividef(static_cast<float>(bin), bins) : hi;
-  return floor_of(value, hi);
+  const float value = scale > 0.f ? hi - __fdividef(static_cast<float>(rank.bin + 1), scale) : hi;
+  return floor_of(value, most);
 }
 
 // A warp streams four runs of its share of the slice at once, a vector of each per step, so that its first loads

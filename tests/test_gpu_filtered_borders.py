@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_filtered import S, check  # noqa: F401
+from test_gpu_filtered import S, check, filters_of, on_gpu  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 V = 262144
@@ -66,3 +66,38 @@ def test_weights_below_the_smallest_unit_do_not_count(S, copies, u):
     got = S.sample_filtered(logits, uu, 1.0, 0, torch.tensor(p, device="cuda"), 0.0)
     tokens = check(S, logits[-n:], uu[-n:], np.ones(n), np.zeros(n, int), p[-n:], np.zeros(n), [t[-n:] for t in got], 0)
     assert (tokens == 600).all() and all(torch.equal(t, t[-n:].repeat(copies)) for t in got)
+
+
+@pytest.mark.parametrize("R", [3, 100, 330])  # eight to one CTA per row
+@pytest.mark.parametrize("mask", [-1e4, -1e9, "lowest"])
+@pytest.mark.parametrize("kind", ["block", "ends", "allowed", "few", "one", "levels"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_masked_by_finite_values(S, R, mask, kind, dtype):
+    # the estimate that a row is streamed with must not take the mask's distance for the spread of its logits
+    n, few = 40000, 6
+    g = torch.Generator(device="cuda").manual_seed(R)
+    x = (2.5 * torch.randn(R, n, device="cuda", generator=g)).to(dtype)
+    low = torch.finfo(dtype).min if mask == "lowest" else mask
+    if kind == "block":
+        x[:, 9000:30000] = low
+    elif kind == "ends":
+        x[:, :8000] = low
+        x[:, -15000:] = low
+    elif kind == "levels":  # masks of several depths
+        x[:, 5000:9000] = -50.0
+        x[:, 9000:20000] = low
+        x[:, 20000:33000] -= 300.0
+    else:  # so many tokens are allowed, at places of each row's own
+        allowed = {"allowed": 3000, "few": 300, "one": 1}[kind]
+        at = torch.rand(R, n, device="cuda", generator=g).topk(allowed, dim=1).indices
+        x = torch.full_like(x, low).scatter_(1, at, x.gather(1, at))
+    u = torch.rand(R, device="cuda", generator=g)
+    for kinds in ("k", "p", "k_p", "m", "none", "mixed"):
+        T, k, p, m = filters_of(R, 7, kinds)
+        got = S.sample_filtered(x, u, *on_gpu(T, k, p, m))
+        check(S, x[-few:], u[-few:], T[-few:], k[-few:], p[-few:], m[-few:], [t[-few:] for t in got])
+    for k in (1, 64, 700):
+        v, i, _ = S.top_logits(x, k)
+        want = torch.sort(x[-few:].float(), dim=1, descending=True, stable=True)
+        assert torch.equal(v[-few:], want.values[:, :k]) and torch.equal(i[-few:].long(), want.indices[:, :k])
+    assert S.check_status() == 0
