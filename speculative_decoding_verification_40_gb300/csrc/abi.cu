@@ -713,6 +713,14 @@ int spec_check_status(void* workspace, void* stream) {
     cudaGetLastError();
     return SPEC_ERR_CUDA;
   }
+#ifdef SPEC_DEBUG_BOUNDS
+  uint32_t filtered = 0, distill = 0;
+  if (specv::filtered_bounds(&filtered) != cudaSuccess || specv::distill_bounds(&distill) != cudaSuccess) {
+    cudaGetLastError();
+    return SPEC_ERR_CUDA;
+  }
+  if (filtered | distill) return SPEC_ERR_BOUNDS;
+#endif
   if (word == 0) return SPEC_OK;
   if (cudaMemsetAsync(workspace, 0, sizeof(word), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess) {
     cudaGetLastError();

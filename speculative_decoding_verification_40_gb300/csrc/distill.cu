@@ -20,6 +20,7 @@
 #include "../../include/spec_verify.h"
 #include "common.cuh"
 #include "pair.cuh"
+#include "row_bounds.cuh"
 #include "row_kernels.h"
 #include "softmax.cuh"
 
@@ -530,6 +531,7 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
   const int32_t* ids = p.ids + static_cast<size_t>(r) * p.K;
   const float* values = p.values + static_cast<size_t>(r) * p.K;
   const Slice<T> s(row, p.V, rank, split);
+  if (!index_ok(r < p.N && split <= kDSplit && s.per * split >= s.nv && s.head + s.nv * kV <= p.V)) return;
   Entry* entries = reinterpret_cast<Entry*>(raw + shared_bytes());
   uint32_t* bits = reinterpret_cast<uint32_t*>(raw + shared_bytes() + entry_bytes(p.K));
   uint32_t* hits = bits + bitmap_bytes(s.per, kV) / 4;
@@ -574,11 +576,11 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
       if (id != -1) {
         bad |= id < 0 || id >= p.V || !(v < INFINITY);
         const int b = id >= 0 && id < p.V ? s.bit(id) : -1;
-        mine = b >= 0;
+        mine = b >= 0 && index_ok(b < s.per * kV + 16);
         if (mine) {
           twice |= (atomicOr(bits + (b >> 5), 1u << (b & 31)) >> (b & 31)) & 1u;
           const int v = b / kV, group = v / (kT * kDU);
-          if (v < s.per) atomicOr(hits + group / 32 * kT + v % kT, 1u << (group % 32));
+          if (v < s.per && index_ok(group / 32 < hit_words(s.per, kT))) atomicOr(hits + group / 32 * kT + v % kT, 1u << (group % 32));
         }
       }
     }
@@ -628,8 +630,9 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
       const int base = __shfl_sync(0xffffffffu, incl - mine, i * kW + warp);
       if (is) {
         const int k = i * kT + tid;
-        entries[base + __popc(all & ((1u << lane) - 1u))] =
-            i == 0 ? Entry{v0, 0.f, 0.f, id0} : Entry{values[k], 0.f, 0.f, ids[k]};
+        const int at = base + __popc(all & ((1u << lane) - 1u));
+        if (index_ok(at < n && at < p.K))
+          entries[at] = i == 0 ? Entry{v0, 0.f, 0.f, id0} : Entry{values[k], 0.f, 0.f, ids[k]};
       }
     }
   }
@@ -641,7 +644,9 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
     const Scale w(c, ref);
     flags |= twice;
     // the first entry's logit is on its way while the slice is streamed
-    const float logit = again == 0 && tid < n ? Elems<T>::one(row, entries[tid].id) : 0.f;
+    const float logit = again == 0 && tid < n && index_ok(entries[tid].id >= 0 && entries[tid].id < p.V)
+                            ? Elems<T>::one(row, entries[tid].id)
+                            : 0.f;
     if (kGrad && again == 0) kept_wait<0>();
     Pair sum{0.f, 0.f};
     if (some_rest) sum = warp_sum(w.clean(sum_slice<T, kT, kGrad>(row, p.V, s, bits, hits, first, w, kept)));
@@ -651,6 +656,7 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
       Pair mass{0.f, 0.f}, against{0.f, 0.f}, top{0.f, 0.f};
       for (int i = tid; i < n; i += kT) {
         Entry e = entries[i];
+        if (!index_ok(e.id >= 0 && e.id < p.V && i < p.K)) continue;
         if (again == 0) e.l = i < kT ? logit : Elems<T>::one(row, e.id);
         const Pair x = entry_log(rec, e.v);
         const Pair pr = probability(x);
@@ -784,7 +790,7 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
   const Scale w_in(c, sh.ref_in);
   for (int i = tid; i < n; i += kT) {
     const Entry e = entries[i];
-    out[e.id] = to_grad<T>(__fmaf_rn(w_in(e.l), k_in, -__fmul_rn(e.p, scale)));
+    if (index_ok(e.id >= 0 && e.id < p.V)) out[e.id] = to_grad<T>(__fmaf_rn(w_in(e.l), k_in, -__fmul_rn(e.p, scale)));
   }
 }
 
@@ -801,6 +807,7 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   const T* row = static_cast<const T*>(p.student) + static_cast<size_t>(r) * p.V;
   T* out = static_cast<T*>(p.grad) + static_cast<size_t>(r) * p.V;
   const Slice<T> s(row, p.V, rank, split);
+  if (!index_ok(r < p.N && s.per * split >= s.nv)) return;
   const float g = p.grad_loss ? p.grad_loss[r] : 1.f;
   const int32_t* ids = p.ids + static_cast<size_t>(r) * p.K;
   const float* values = p.values + static_cast<size_t>(r) * p.K;
@@ -868,7 +875,7 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   __syncthreads();
   for (int k = tid; k < p.K; k += kDT) {  // the slice's tokens of the record, over what was written there
     const int id = ids[k];
-    if (id < 0 || s.bit(id) < 0) continue;
+    if (id < 0 || s.bit(id) < 0 || !index_ok(id < p.V)) continue;
     const float pk = values[k] > -INFINITY ? value(probability(entry_log(rec, values[k]))) : 0.f;
     out[id] = to_grad<T>(__fmaf_rn(w_in(Elems<T>::one(row, id)), k_in, -__fmul_rn(pk, scale)));
   }
@@ -934,6 +941,10 @@ cudaError_t launch_backward(const DistillParams& p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+#ifdef SPEC_DEBUG_BOUNDS
+cudaError_t distill_bounds(uint32_t* word) { return take_row_bounds(word); }
+#endif
 
 cudaError_t distill_forward_launch(const DistillParams& p, int dtype, cudaStream_t stream) {
   return dtype == 0 ? launch_loss<float, false>(p, stream) : launch_loss<__nv_bfloat16, false>(p, stream);

@@ -22,6 +22,7 @@
 
 #include "../../include/spec_verify.h"
 #include "common.cuh"
+#include "row_bounds.cuh"
 #include "row_kernels.h"
 #include "select.cuh"
 #include "softmax.cuh"
@@ -280,6 +281,7 @@ __device__ CutResult select_key(const S& src, uint32_t lo, uint32_t hi, unsigned
     });
     __syncthreads();
     const Pick p = pick_from_top<kFT>(h, kNB, need - above, sh.wsum, &sh.pick);
+    if (!index_ok(p.bin >= 0 && p.bin < kNB)) return CutResult{hi, above, 0ull};
     above += p.above;
     lo += static_cast<uint32_t>(p.bin) << shift;
     if (shift == 0) {
@@ -386,6 +388,7 @@ __device__ int draw_from_groups(float u, Shared& sh, unsigned long long* total, 
   sh.draw.token[tid + kFT] = 0ull;
   __syncthreads();
   const int g = sh.at;
+  if (!index_ok(g >= 0 && g < kGroups)) return -1;
   fill(g);
   __syncthreads();
   a = sh.draw.token[2 * tid];
@@ -425,7 +428,7 @@ __device__ __forceinline__ unsigned long long draw_unit(unsigned long long w, fl
 // Draws from the list's logits with key >= tau: the smallest token whose running weight exceeds u * total.
 template <typename T>
 __device__ void draw_from_list(const ListSource& src, uint32_t tau, const Weight& weight, const RowFilter& f,
-                               Shared& sh, const T* row, const RowOut& out) {
+                               Shared& sh, const T* row, int V, const RowOut& out) {
   const int tid = threadIdx.x;
   unsigned int least = 0xffffffffu;
   __syncthreads();
@@ -470,7 +473,7 @@ __device__ void draw_from_list(const ListSource& src, uint32_t tau, const Weight
     const uint32_t key = fkey(l);
     if (key < tau) return;
     least = min(least, key);
-    groups.add(id / kGroup, draw_unit(sh.w[i], l, weight, f.u));
+    if (index_ok(id >= 0 && id < kMaxVocab)) groups.add(id / kGroup, draw_unit(sh.w[i], l, weight, f.u));
   });
   least = __reduce_min_sync(0xffffffffu, least);
   if ((tid & 31) == 0) atomicMin(&sh.least, least);
@@ -483,7 +486,8 @@ __device__ void draw_from_list(const ListSource& src, uint32_t tau, const Weight
       if (id / kGroup == g && fkey(l) >= tau) sh.draw.token[id % kGroup] = draw_unit(sh.w[i], l, weight, f.u);
     });
   });
-  if (token >= 0) write_drawn(out, f, token, Elems<T>::one(row, token), weight.M, key_float(sh.least), total);
+  if (token >= 0 && index_ok(token < V))
+    write_drawn(out, f, token, Elems<T>::one(row, token), weight.M, key_float(sh.least), total);
 }
 
 // The eight logits a lane holds of half a group of 512 tokens, as they lie in memory (-inf beyond the row).
@@ -558,7 +562,7 @@ __device__ __noinline__ unsigned int sum_groups(const T* row, int V, int g0, int
              },
              [&](int g) {
                sum = warp_sum_u64(sum);
-               if ((threadIdx.x & 31) == 0) dsmem_st_u64(sums + 8 * g, sum);
+               if ((threadIdx.x & 31) == 0 && index_ok(g < kGroups)) dsmem_st_u64(sums + 8 * g, sum);
                sum = 0;
              });
   return least;
@@ -611,7 +615,7 @@ __device__ __noinline__ unsigned long long bracket_groups(const T* row, int V, i
 #pragma unroll
                  for (int j = 0; j < 8; ++j) {
                    const unsigned int is = (keep >> (7 - j)) & 1u;
-                   if (is) gathered[at] = v[j];
+                   if (is && index_ok(at < kGroup)) gathered[at] = v[j];
                    at += is;
                  }
                }
@@ -623,7 +627,7 @@ __device__ __noinline__ unsigned long long bracket_groups(const T* row, int V, i
                    do {
                      const int j = __clz(list) - 24;
                      list &= ~(128u >> j);
-                     sh.id[at++] = Half<T>::token(h, j, lane);
+                     if (index_ok(at < kListCap && Half<T>::token(h, j, lane) < V)) sh.id[at++] = Half<T>::token(h, j, lane);
                    } while (list);
                  }
                }
@@ -643,7 +647,7 @@ __device__ __noinline__ unsigned long long bracket_groups(const T* row, int V, i
                  sum = warp_sum_u64(sum);
                  kept = 0;
                }
-               if (lane == 0) dsmem_st_u64(sums + 8 * g, sum);
+               if (lane == 0 && index_ok(g < kGroups)) dsmem_st_u64(sums + 8 * g, sum);
              });
   return __float2ull_rn(__fmul_rn(tail, kRestOne)) + __float2ll_rn(__fmul_rn(comp, kRestOne));
 }
@@ -662,7 +666,8 @@ __device__ void draw_from_row(const T* row, int V, uint32_t tau, const Weight& w
       if (fkey(l) >= tau) sh.draw.token[i] = draw_unit(weight(l), l, weight, f.u);
     }
   });
-  if (token >= 0) write_drawn(out, f, token, Elems<T>::one(row, token), weight.M, key_float(least), total);
+  if (token >= 0 && index_ok(token < V))
+    write_drawn(out, f, token, Elems<T>::one(row, token), weight.M, key_float(least), total);
 }
 
 // ---------------------------------------------------------------- one pass over a row
@@ -723,6 +728,7 @@ __device__ __forceinline__ SampleRank sample_rank(const Shared& sh, int want) {
   int run = __shfl_sync(0xffffffffu, incl - mine, who), bin = who * kPer;
 #pragma unroll 1
   for (;; ++bin) {
+    if (!index_ok(bin < kSampleBins)) return SampleRank{-1, 0, 0};
     const int in = sh.sample.count[bin];
     if (run + in >= want) return SampleRank{bin, run, in};
     run += in;
@@ -914,7 +920,7 @@ __device__ __forceinline__ void stream_step(const uint4 (&r)[kU], int token, int
       do {
         const int e = __clz(push) - (32 - kN);  // element of the step
         push &= ~(1u << (kN - 1 - e));
-        sh.id[at++] = token + e / kV * apart + e % kV;
+        if (index_ok(at < kListCap)) sh.id[at++] = token + e / kV * apart + e % kV;
       } while (push);
     }
   }
@@ -983,11 +989,12 @@ __device__ float stream(const T* row, int V, const Slice& s, Stream<T>& q, int a
 // The list's logits from its tokens, and the largest of them: NaN or +inf if the row holds one.  The smallest
 // goes to sh.bottom.
 template <typename T>
-__device__ float gather_list(const T* row, Shared& sh) {
+__device__ float gather_list(const T* row, int V, Shared& sh) {
   const int n = sh.n;
   float m = -INFINITY, least = INFINITY;
 #pragma unroll 4
   for (int i = threadIdx.x; i < n; i += kFT) {
+    if (!index_ok(i < kListCap && sh.id[i] >= 0 && sh.id[i] < V)) continue;
     const float l = Elems<T>::one(row, sh.id[i]);
     sh.val[i] = l;
     m = max_nan(m, l);
@@ -1319,7 +1326,7 @@ __device__ Next sample_from_list(const T* row, int V, const Weight& weight, cons
   }
   if (!cut && beyond) return place_bracket(row, V, sh.below, phi, weight, f.t, sh) ? kSecond : kWhole;
   if (!cut) return kWhole;
-  draw_from_list(src, tau, weight, f, sh, row, out);
+  draw_from_list(src, tau, weight, f, sh, row, V, out);
   return kDone;
 }
 
@@ -1391,7 +1398,7 @@ __device__ bool second_pass(const T* row, int V, const Slice& s, uint32_t key_lo
   if (nucleus) {
     if (sh.n > kListCap) return false;
     const ListSource src{sh.val, sh.id, sh.n};
-    gather_list(row, sh);
+    gather_list(row, V, sh);
     unsigned long long mass = 0, above = 0, left, most;
     const ValueBins bins(key_float(key_hi), key_float(key_lo));
     const Hist masses{sh.hist.lo, sh.hist.mid, sh.hist.hi};
@@ -1486,6 +1493,7 @@ __global__ void __launch_bounds__(kFT, 4) sample_filtered_kernel(FilterParams q)
   RowFilter f;
   const bool valid = load_filter(q, r, f);
   const Slice s = slice_of(row, V, rank, split);
+  if (!index_ok(r < q.R && split <= kMaxSplit && (V + kGroup - 1) / kGroup <= kGroups)) return;
   Stream<T> first(row, s);
   const float2 entry = exp2_table_entry();
   if (tid == 0) sh.n = 0;
@@ -1524,7 +1532,7 @@ __global__ void __launch_bounds__(kFT, 4) sample_filtered_kernel(FilterParams q)
         M = sh.most[0];
         for (int i = 1; i < split; ++i) M = max_nan(M, sh.most[i]);
       } else {
-        M = sh.n <= kListCap ? gather_list(row, sh) : row_max(row, V, sh);
+        M = sh.n <= kListCap ? gather_list(row, V, sh) : row_max(row, V, sh);
       }
       weight.M = M;
       if (!(M > -INFINITY && M < INFINITY)) {
@@ -1655,7 +1663,7 @@ __device__ void write_top(const S& src, uint32_t tau, unsigned int last, int m, 
     const uint32_t key = fkey(l);
     if (key > tau || (key == tau && static_cast<unsigned int>(id) <= last)) {
       const int at = atomicAdd(&sh.at, 1);
-      if (at < m) sh.pairs[at] = (static_cast<unsigned long long>(key) << 32) | (0xffffffffu - id);
+      if (at < m && index_ok(at < kBins)) sh.pairs[at] = (static_cast<unsigned long long>(key) << 32) | (0xffffffffu - id);
     }
   });
   __syncthreads();
@@ -1731,6 +1739,7 @@ __global__ void __launch_bounds__(kFT, 4) top_logits_kernel(TopParams q) {
   const int K = q.K, V = q.V;
   const T* row = static_cast<const T*>(q.logits) + static_cast<size_t>(r) * V;
   const Slice s = slice_of(row, V, rank, split);
+  if (!index_ok(r < q.R && split <= kMaxSplit && (V + kGroup - 1) / kGroup <= kGroups)) return;
   Stream<T> first(row, s);
   const float2 entry = exp2_table_entry();
   if (tid == 0) sh.n = 0;
@@ -1775,7 +1784,7 @@ __global__ void __launch_bounds__(kFT, 4) top_logits_kernel(TopParams q) {
   const bool all = n <= kListCap;  // the list holds every logit from the estimate up
   const ListSource src{sh.val, sh.id, n};
   const float below = sh.below;
-  const float M = all ? gather_list(row, sh) : row_max(row, V, sh);
+  const float M = all ? gather_list(row, V, sh) : row_max(row, V, sh);
   if (!(M > -INFINITY && M < INFINITY)) {
     for (int i = tid; i < K; i += kFT) {
       values[i] = NAN;
@@ -1864,6 +1873,10 @@ static cudaError_t launch_rows(void (*kernel)(P), std::atomic<unsigned long long
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
+
+#ifdef SPEC_DEBUG_BOUNDS
+cudaError_t filtered_bounds(uint32_t* word) { return take_row_bounds(word); }
+#endif
 
 // Sampling: up to 27 CTAs per eight SMs (513 on 152), since a row's second pass is the faster the more CTAs share it
 // (rows of 128256 with mixed filters: 64 of them 63 us with eight CTAs per row, 81 with two, 134 with one; 150 75 us

@@ -59,4 +59,10 @@ cudaError_t distill_forward_launch(const DistillParams& p, int dtype, cudaStream
 cudaError_t distill_backward_launch(const DistillParams& p, int dtype, cudaStream_t stream);
 cudaError_t distill_loss_grad_launch(const DistillParams& p, int dtype, cudaStream_t stream);
 
+#ifdef SPEC_DEBUG_BOUNDS
+// what the kernels' index checks recorded (0: nothing), which is cleared
+cudaError_t filtered_bounds(uint32_t* word);
+cudaError_t distill_bounds(uint32_t* word);
+#endif
+
 }  // namespace specv
