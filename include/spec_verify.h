@@ -330,7 +330,8 @@ int spec_sample_filtered(const void* logits, int dtype, const float* uniforms, c
  *   values  [R, K]  float32 out, descending; equal logits in the order of their tokens; -inf beyond the
  *                   row's finite logits
  *   ids     [R, K]  int32 out: their tokens, -1 beyond the row's finite logits
- *   lse     [R]     float32 out: ln sum_x exp(l(x) / T); may be NULL
+ *   lse     [R]     float32 out: ln sum_x exp(l(x) / T) (infinite where the largest logit over T is no
+ *                   float32); may be NULL
  * temperature in [2^-64, 2^64].  A row that holds NaN or +inf or only -inf gets
  * values NaN, ids -1 and lse NaN.  No workspace; nothing is kept between calls. */
 int spec_top_logits(const void* logits, int dtype, float temperature, int R, int V, int K,

@@ -1810,7 +1810,8 @@ __global__ void __launch_bounds__(kFT, 4) top_logits_kernel(TopParams q) {
       }
       // M / T and its remainder, and ln of the sum relative to the largest weight
       const float s = __fdiv_rn(M, q.temperature);
-      q.lse[r] = s + (log_weight(total) + __fdiv_rn(__fmaf_rn(-s, q.temperature, M), q.temperature));
+      const float rest = log_weight(total) + __fdiv_rn(__fmaf_rn(-s, q.temperature, M), q.temperature);
+      q.lse[r] = fabsf(s) < INFINITY ? s + rest : s;
     }
   }
   if (all && (n >= K || below == -INFINITY)) {

@@ -101,3 +101,16 @@ def test_rows_masked_by_finite_values(S, R, mask, kind, dtype):
         want = torch.sort(x[-few:].float(), dim=1, descending=True, stable=True)
         assert torch.equal(v[-few:], want.values[:, :k]) and torch.equal(i[-few:].long(), want.indices[:, :k])
     assert S.check_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_log_sum_exp_past_the_range_of_float32(S, dtype):
+    # the largest logit over T leaves float32: the log-sum-exp is infinite with its sign, the record as ever
+    x = torch.full((4, 5000), -1e30, device="cuda", dtype=dtype)
+    x[0, 7] = 3e30
+    x[1, 9] = -2e29
+    x[2, 11] = 100.0
+    x[3] = torch.finfo(dtype).min
+    v, i, lse = S.top_logits(x, 1, 2.0 ** -40)
+    assert v[:, 0].tolist() == x.float().amax(1).tolist() and i[:, 0].tolist() == [7, 9, 11, 0]
+    assert lse.tolist() == [float("inf"), -float("inf"), 2.0 ** 40 * 100, -float("inf")]
