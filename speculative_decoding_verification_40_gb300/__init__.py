@@ -430,6 +430,8 @@ def sample_filtered(logits: torch.Tensor, uniforms: torch.Tensor, temperature=1.
     ws = workspace if workspace is not None else _WS.get(("cuda", index))
     if ws is None:
         ws = workspace_for(logits.device, 4096)
+    elif workspace is not None:
+        _checked(ws, "workspace", torch.uint8, ws.shape, index)  # (the kernel writes its error word there)
     _call(index, "spec_sample_filtered", lib.spec_sample_filtered, logits.data_ptr(), code, u, t, k, p, m,
           t0, k0, p0, m0, R, V, tokens.data_ptr(), thr.data_ptr(), logp.data_ptr(), ws.data_ptr(), ws.numel())
     if check:

@@ -114,3 +114,13 @@ def test_log_sum_exp_past_the_range_of_float32(S, dtype):
     v, i, lse = S.top_logits(x, 1, 2.0 ** -40)
     assert v[:, 0].tolist() == x.float().amax(1).tolist() and i[:, 0].tolist() == [7, 9, 11, 0]
     assert lse.tolist() == [float("inf"), -float("inf"), 2.0 ** 40 * 100, -float("inf")]
+
+
+def test_workspaces_that_are_refused(S):
+    # the kernels write the error word: a workspace on the host, of another type or with gaps is refused before the launch
+    x, u = torch.zeros(2, 100, device="cuda"), torch.zeros(2, device="cuda")
+    ok = torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    for bad, error in ((ok.cpu(), ValueError), (ok.int(), TypeError), (ok[::2], ValueError), (ok.cpu().pin_memory(), ValueError)):
+        with pytest.raises(error, match="workspace"):
+            S.sample_filtered(x, u, workspace=bad)
+    assert S.sample_filtered(x, u, workspace=ok, check=True)[0].tolist() == [0, 0]
