@@ -382,6 +382,11 @@ def _logits(t: torch.Tensor, name: str) -> tuple[int, int]:
     return t.get_device(), _dtype_code(t)
 
 
+def _count(k, V: int):
+    """top_k as the library takes it: from V on every count means all (beyond 32 bits it would wrap around)."""
+    return max(-1, min(k, V))
+
+
 def _call(index: int, where: str, fn, *args):
     """fn(*args, stream) with device `index` current, on its current stream."""
     if index == torch._C._cuda_getDevice():
@@ -411,6 +416,8 @@ def sample_filtered(logits: torch.Tensor, uniforms: torch.Tensor, temperature=1.
         t, t0 = _vector(temperature, "temperature", torch.float32, R, index), 1.0
     if isinstance(top_k, torch.Tensor):
         k, k0 = _vector(top_k, "top_k", torch.int32, R, index), 0
+    else:
+        k0 = _count(top_k, V)
     if isinstance(top_p, torch.Tensor):
         p, p0 = _vector(top_p, "top_p", torch.float32, R, index), 1.0
     if isinstance(min_p, torch.Tensor):

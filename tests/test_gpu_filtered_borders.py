@@ -124,3 +124,13 @@ def test_workspaces_that_are_refused(S):
         with pytest.raises(error, match="workspace"):
             S.sample_filtered(x, u, workspace=bad)
     assert S.sample_filtered(x, u, workspace=ok, check=True)[0].tolist() == [0, 0]
+
+
+def test_top_k_past_32_bits_keeps_all(S):
+    x = torch.linspace(-3, 0, 5000, device="cuda").repeat(64, 1)
+    u = torch.linspace(0, 0.99, 64, device="cuda")
+    want = S.sample_filtered(x, u)
+    for k in (5000, 2 ** 31, 2 ** 32 + 5, 2 ** 40):
+        assert all(torch.equal(a, b) for a, b in zip(S.sample_filtered(x, u, 1.0, k), want))
+    with pytest.raises(S.SpecVerifyError):
+        S.sample_filtered(x, u, 1.0, -2 ** 32 + 5)
