@@ -156,6 +156,7 @@ def workspace_size(B: int, gamma: int, V: int, dtype: torch.dtype = torch.float3
 
 
 _WS: dict = {}
+_WS_OUTGROWN: list = []  # a captured graph goes on writing into the workspace that it was captured with
 
 
 def workspace_for(device: torch.device, nbytes: int) -> torch.Tensor:
@@ -163,12 +164,15 @@ def workspace_for(device: torch.device, nbytes: int) -> torch.Tensor:
 
     The library leaves every counter it uses at zero after each call, so one
     workspace serves any sequence of calls on one stream; calls that may
-    overlap on the GPU need workspaces of their own (pass `workspace=`).
+    overlap on the GPU need workspaces of their own (pass `workspace=`).  One
+    that has been outgrown stays allocated for the graphs that hold it.
     """
     device = torch.device(device)
     key = (device.type, device.index if device.index is not None else torch.cuda.current_device())
     ws = _WS.get(key)
     if ws is None or ws.numel() < nbytes:
+        if ws is not None:
+            _WS_OUTGROWN.append(ws)
         ws = torch.zeros(max(nbytes, 4096), dtype=torch.uint8, device=device)
         _WS[key] = ws
     return ws
