@@ -372,9 +372,12 @@ int spec_top_logits(const void* logits, int dtype, float temperature, int R, int
  * only -inf, or if its record holds a token outside [0, V), a token twice, a
  * value NaN or +inf, no finite value where teacher_lse is NULL, or a lse that
  * is not finite: its loss, stats and gradient are NaN (the backward pass takes
- * a token twice and the logits' state from the stats).  The stats are float32: where
- * the largest logit over T is none (3.4e38 / 0.7), they are infinite, and the
- * backward pass gives NaN.
+ * a token twice and the logits' state from the stats).  The stats are float32, and
+ * the backward pass's weights are exact to 2^-24 of them: from a log-sum-exp of
+ * 2^22 on (a T too small for the logits) its gradient is NaN, and where that
+ * outside the record lies beyond -2^22 (a mask by the type's lowest value) the
+ * tail's part of the gradient is left out; spec_distill_loss_grad goes by the
+ * logits themselves.
  * spec_distill_loss_grad is the forward and the backward pass at once: a
  * training step whose grad_loss is known beforehand.  No workspace; nothing is
  * kept between calls.  Host-side errors as for the other entry points. */

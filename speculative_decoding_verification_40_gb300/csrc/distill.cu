@@ -234,20 +234,27 @@ __host__ __device__ inline int bitmap_bytes(int per, int kV) { return (per * kV 
 
 __host__ __device__ inline int entry_bytes(int K) { return (K * static_cast<int>(sizeof(Entry)) + 15) / 16 * 16; }
 
+// exp(-x) of what the roundings of a scale miss: next to nothing but for logits of 10^4 T and more.
+__device__ __forceinline__ Pair make_up(float x) {
+  return fabsf(x) < 0.00195f ? Pair{1.f, __fmaf_rn(0.5f * x, x, -x)} : Pair{expf(-x), 0.f};
+}
+
 // Weights 2^(s c + shift), shift the float32 nearest to -ref c: one FFMA and one exponential a logit.  They stand
-// for 2^((s - ref) c) times 1 + miss, the product's own rounding, which is taken out of their sums.  A reference of 1e30
-// and more (a mask by the type's lowest value) could leave float32's range with c; logits of that size differ by 2^76 or
-// nothing, so that any power of two in the place of c says the same for every T, without a rounding.
+// for 2^((s - ref) c) times e^miss, the product's own rounding, which is taken out of their sums.  Where the product is
+// 2^31 and more (a small T, a mask by the type's lowest value), two logits next to ref are 2^64 apart in weight or one
+// value, so that a power of two in the place of c that keeps the product exact, and any two apart by 2^512, says the
+// same.
 struct Scale {
-  float c, ref, shift, miss;
-  __device__ __forceinline__ Scale(float c_, float ref_) {
-    c = fabsf(ref_) < 1e30f ? c_ : 0.0009765625f;
-    ref = ref_;
+  float c, shift, miss;
+  __device__ __forceinline__ Scale(float c_, float ref) {
+    c = c_;
+    if (!(fabsf(__fmul_rn(ref, c)) < 2147483648.f))
+      c = __uint_as_float((288u << 23) - (__float_as_uint(ref) & 0x7f800000u));  // 2^34 by ref's own power of two
     shift = -__fmul_rn(ref, c);
     miss = __fmul_rn(__fmaf_rn(ref, c, shift), kLn2Hi);
   }
   __device__ __forceinline__ float operator()(float s) const { return fast_exp2(__fmaf_rn(s, c, shift)); }
-  __device__ __forceinline__ Pair clean(const Pair& sum) const { return sum * Pair{1.f, -miss}; }
+  __device__ __forceinline__ Pair clean(const Pair& sum) const { return sum * make_up(miss); }
 };
 
 // Adds the weights of a vector's elements outside the record (bits: which are in it) to acc, two at a time.
@@ -744,8 +751,8 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
         const float scale = __fmul_rn(g, p.inv_t), f = again ? 1.f : f_out;
         const float share = tail > 0.f && rest > 0.f ? __fdividef(__fmul_rn(tail, f), rest) : 0.f;
         if (lane == rank) {
-          sh.k_in = __fdividef(__fmul_rn(both, f_in), total) * __fmul_rn(scale, 1.f - Scale(c, sh.ref_in).miss);
-          sh.k_out = (any & 1) ? NAN : (__fdividef(__fmul_rn(both, f_out), total) - share) * __fmul_rn(scale, 1.f - w.miss);
+          sh.k_in = __fdividef(__fmul_rn(both, f_in), total) * __fmul_rn(scale, value(make_up(Scale(c, sh.ref_in).miss)));
+          sh.k_out = (any & 1) ? NAN : (__fdividef(__fmul_rn(both, f_out), total) - share) * __fmul_rn(scale, value(make_up(w.miss)));
         }
       }
       const bool redo = __any_sync(0xffffffffu, far) || !(rest >= kLeastRest);
@@ -796,6 +803,9 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
 
 // ---------------------------------------------------------------- gradient from the forward pass's stats
 
+// A float32 log-sum-exp tells the weights relative to it to 2^-24 of itself, nothing from here up.
+constexpr float kTelling = 4194304.f;  // 2^22
+
 // One read and one write of the row: q_j needs the two statistics and nothing of the row's other logits, so a row's CTAs
 // know nothing of each other.  Bound by DRAM: 1536 x 152064 float32, record of 64, 292 us (6.4 TB/s read and
 // written, 94 % of the copy peak); 64 x 32128 float32 7.5 us.
@@ -839,7 +849,7 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   for (int k = tid; k < p.K; k += kDT)
     if (ids[k] >= 0 && values[k] > -INFINITY) mass = mass + probability(entry_log(rec, values[k]));
   mass = block_sum<kDT>(mass, part);
-  bad |= !(fabsf(lse) < INFINITY);  // the forward pass found the row invalid
+  bad |= !(fabsf(lse) < kTelling);  // the forward pass found the row invalid, or its statistics tell nothing
   bad = __syncthreads_or(bad);
   const float gap = lse - lse_rest;
   const float tail = p.teacher_lse ? beyond(mass, teacher_lse, gap) : 0.f;
@@ -849,14 +859,14 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   auto scale_of = [&](float lse, float& k) {
     const float ref = __fmul_rn(lse, p.temperature);
     const Scale w(p.c, ref);
-    k = scale * (1.f - (w.miss + __fmul_rn(__fmaf_rn(lse, p.temperature, -ref), p.inv_t)));  // (lse - ref / T)
+    k = scale * value(make_up(w.miss + __fmul_rn(__fmaf_rn(lse, p.temperature, -ref), p.inv_t)));  // (lse - ref / T)
     return w;
   };
   // tokens outside the record: q less their share of the tail, relative to lse, or to lse_rest where that is so far
   // below that q is nothing and the quotient of the two would leave float32's range
-  const bool apart = gap > 40.f && gap < INFINITY;
+  const bool apart = gap > 40.f && fabsf(lse_rest) < kTelling;
   const float ratio = exp_pair(two_sum(apart ? lse_rest : lse, apart ? -lse : -lse_rest));
-  const float share = tail > 0.f && lse_rest > -INFINITY ? tail * (apart ? 1.f : ratio) : 0.f;
+  const float share = tail > 0.f && fabsf(lse_rest) < kTelling ? tail * (apart ? 1.f : ratio) : 0.f;
   float k_in, k;
   const Scale w_in = scale_of(lse, k_in), w = scale_of(apart ? lse_rest : lse, k);
   k_in *= both;
