@@ -361,7 +361,8 @@ int spec_top_logits(const void* logits, int dtype, float temperature, int R, int
  *   ids        [N, K]  int32: distinct tokens, or -1; in any order
  *   loss       [N]     float32 out
  *   stats      [N, 2]  float32 out of the forward pass, in of the backward pass: the log-sum-exp of
- *                      student / T over the vocabulary, and over the tokens outside the record
+ *                      student / T over the vocabulary, and over the tokens outside the record (which may be
+ *                      -inf where those hold less than e^-87 of the whole and the teacher's r is 0)
  *   grad_loss  [N]     float32: dL/dloss; NULL: 1 for every row
  *   grad       [N, V]  dtype, out: grad_loss[n] * dloss[n]/dstudent[n, :], rounded once; it may not overlap
  *                      student

@@ -745,7 +745,8 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
         }
         // a token of the record has q = weight f_in / total, f_in the step from its reference to the common one; any
         // other weighs f_out / total in the row and f / rest in the tail
-        const float gap = again ? (most - sh.ref_out) * p.inv_t - logf(__fdividef(rest, total)) : 0.f;
+        const float gap = again ? (most - sh.ref_out) * p.inv_t - logf(__fdividef(rest, total))
+                          : rest > 0.f ? 0.f : INFINITY;
         const float tail = p.teacher_lse ? beyond(mass, p.teacher_lse[r], gap) : 0.f, both = value(mass) + tail;
         // (approximate quotients, two steps of 2^-23: their operands' weights carry the exponential's 2^-22 each)
         const float scale = __fmul_rn(g, p.inv_t), f = again ? 1.f : f_out;
@@ -755,7 +756,20 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
           sh.k_out = (any & 1) ? NAN : (__fdividef(__fmul_rn(both, f_out), total) - share) * __fmul_rn(scale, value(make_up(w.miss)));
         }
       }
-      const bool redo = __any_sync(0xffffffffu, far) || !(rest >= kLeastRest);
+      bool redo = __any_sync(0xffffffffu, far);
+      if (!(rest >= kLeastRest)) {
+        // no weight outside the record at all: nothing to know of it where the teacher has no mass there either (both
+        // models' vocabularies constrained alike: 2304 x 128256 bf16 108 us, 238 with a second pass)
+        Pair mass{0.f, 0.f};
+        float top = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < split; ++i) {
+          mass = mass + sh.parts[i].mass;
+          top += value(sh.parts[i].top) * step(sh.parts[i].ref, most, c);
+        }
+        const float tail = p.teacher_lse ? beyond(mass, p.teacher_lse[r], INFINITY) : 0.f;
+        redo |= rest != 0.f || tail > 0.f || !(top >= kLeastRest);
+      }
       if (lane == 0) {
         sh.most = most;
         sh.flags = any;

@@ -90,7 +90,8 @@ def check(S, student, v, i, T, lse, rows=None, stats=None):
             assert x == L or (L > most * (1 - HALF) and x == np.inf) or abs(x - L) <= tl + HALF * min(L, most), (n, x, L, tl)
         got = st[n].tolist()
         for x, y in zip(got, w["stats"]):
-            assert x == y or (y < -most and x == -np.inf) or abs(x - y) <= a + HALF * abs(y), (n, got, w["stats"])
+            nothing = y < -most or (r == 0 and w["gap"] > 87 and y == w["stats"][1])
+            assert x == y or (nothing and x == -np.inf) or abs(x - y) <= a + HALF * abs(y), (n, got, w["stats"])
         rel = lambda x: 2 * a + 6 * HALF * np.where(np.isfinite(x), np.abs(x), 0.0) + 2.0 ** -20  # noqa: E731
         for k, x in enumerate((grad, grad2)):
             held = 2 * HALF * np.abs(w["stats"][0 if r == 0 or np.isinf(gap) else [0, 1]]).sum() if k == 0 else 0.0
