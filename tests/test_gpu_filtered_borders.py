@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_filtered import S, check, filters_of, on_gpu  # noqa: F401
+from test_gpu_filtered import S, check, filters_of, logits_of, on_gpu  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 V = 262144
@@ -134,3 +134,18 @@ def test_top_k_past_32_bits_keeps_all(S):
         assert all(torch.equal(a, b) for a, b in zip(S.sample_filtered(x, u, 1.0, k), want))
     with pytest.raises(S.SpecVerifyError):
         S.sample_filtered(x, u, 1.0, -2 ** 32 + 5)
+
+
+@pytest.mark.parametrize("R", [4, 330])
+@pytest.mark.parametrize("T", [2.0 ** -64, 1e-4, 50.0, 2.0 ** 64])
+@pytest.mark.parametrize("shift", [0.0, -1e6])
+def test_long_rows_at_extreme_temperatures_and_far_from_zero(S, R, T, shift):
+    n, few = 40000, 4
+    x = logits_of(R, n, "f32", 31) + shift
+    u = torch.rand(R, device="cuda", generator=torch.Generator(device="cuda").manual_seed(9))
+    for kinds in ("k", "p", "k_p", "m", "none"):
+        _, k, p, m = filters_of(R, 8, kinds)
+        t = np.full(R, T)
+        got = S.sample_filtered(x, u, *on_gpu(t, k, p, m))
+        check(S, x[-few:], u[-few:], t[-few:], k[-few:], p[-few:], m[-few:], [y[-few:] for y in got])
+    assert S.check_status() == 0
