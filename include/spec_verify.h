@@ -280,6 +280,9 @@ int spec_sample_rows_masked(const void* logits, int dtype, const float* uniforms
                             float temperature, int R, int V, int32_t* tokens,
                             void* workspace, size_t ws_bytes, void* stream);
 
+/* Filtered sampling, top logits and distillation: rows may start anywhere, but a
+ * pointer that is no multiple of its element's size returns SPEC_ERR_ARG. */
+
 /* The draft-side sampler with a request's own parameters: temperature, top-k,
  * top-p and min-p per row, and one given uniform number.  For each row r of
  * `logits`, with M its largest logit, T = temperature[r] and the weights

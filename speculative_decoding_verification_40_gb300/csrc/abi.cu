@@ -340,6 +340,13 @@ int launch_status(cudaError_t e) {
 // scale log2(e) / T and its rest stay normal float32.
 bool good_temperature(float t) { return t >= 5.42101086e-20f && t <= 1.84467441e19f; }
 
+// Whether every pointer lies on a multiple of `bytes` (a null one does): the row operators' kernels round a row's address
+// to 16 bytes in elements, so that an element between two multiples would be read across them.
+template <typename... P>
+bool on_multiples(int bytes, P... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & static_cast<uintptr_t>(bytes - 1)) == 0;
+}
+
 // Host-side checks of the distillation entry points, and their kernels' parameters.
 int distill_params(const void* student, int dtype, const float* values, const int32_t* ids, const float* teacher_lse,
                    const float* grad_loss, float temperature, int N, int V, int K, float* loss, float* stats,
@@ -351,6 +358,8 @@ int distill_params(const void* student, int dtype, const float* values, const in
   if (student == nullptr || values == nullptr || ids == nullptr || stats == nullptr) return SPEC_ERR_ARG;
   if ((forward && loss == nullptr) || (backward && grad == nullptr)) return SPEC_ERR_ARG;
   const int esz = dtype == SPEC_F32 ? 4 : 2;
+  if (!on_multiples(esz, student, grad) || !on_multiples(4, values, ids, teacher_lse, grad_loss, loss, stats))
+    return SPEC_ERR_ARG;
   bool vec = true;
   if (backward) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(student), b = reinterpret_cast<uintptr_t>(grad);
@@ -607,6 +616,9 @@ int spec_sample_filtered(const void* logits, int dtype, const float* uniforms, c
   if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 || ws_bytes < 256)
     return SPEC_ERR_WORKSPACE;
   if (logits == nullptr || uniforms == nullptr || tokens == nullptr) return SPEC_ERR_ARG;
+  if (!on_multiples(dtype == SPEC_F32 ? 4 : 2, logits) ||
+      !on_multiples(4, uniforms, temperature, top_k, top_p, min_p, tokens, thr, logp))
+    return SPEC_ERR_ARG;
   specv::FilterParams p = {};
   p.logits = logits;
   p.uniforms = uniforms;
@@ -635,6 +647,7 @@ int spec_top_logits(const void* logits, int dtype, float temperature, int R, int
   if (K < 1 || K > SPEC_MAX_TOP || !good_temperature(temperature)) return SPEC_ERR_ARG;
   if (R == 0) return SPEC_OK;
   if (logits == nullptr || values == nullptr || ids == nullptr) return SPEC_ERR_ARG;
+  if (!on_multiples(dtype == SPEC_F32 ? 4 : 2, logits) || !on_multiples(4, values, ids, lse)) return SPEC_ERR_ARG;
   specv::TopParams p = {};
   p.logits = logits;
   p.temperature = temperature;
