@@ -407,7 +407,7 @@ def sample_filtered(logits: torch.Tensor, uniforms: torch.Tensor, temperature=1.
     """spec_sample_filtered: logits [R, V], uniforms [R] float32; temperature, top_p, min_p (float32) and top_k
     (int32) are numbers or [R] tensors.  Returns (tokens [R] int32, thr [R] float32, logp [R] float32): the drawn
     tokens, the smallest kept logit of each row (a threshold for verify_sample / sample_rows) and the drawn
-    tokens' log-probabilities."""
+    tokens' log-probabilities.  A batch without filters is sample_rows's, in a sixth of the time."""
     if logits.dim() != 2:
         raise ValueError("logits must be [R, V]")
     R, V = logits.shape

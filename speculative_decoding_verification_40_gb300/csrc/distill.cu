@@ -522,9 +522,10 @@ __device__ __noinline__ void write_loss(const DistillParams& p, int r, const Sha
 
 // Loss and statistics of a row, and its gradient (kGrad).  Bound: without the gradient the loads (eight CTAs per SM,
 // 64 registers; half of the issue slots are used); with it the phases of a row (copy, sum, exchange,
-// gradient), which two other CTAs on the SM cover in part, and 11 instructions a logit.  Measured: the loss of
-// 2304 x 128256 bf16, record of 64, 99 us (6.0 TB/s), 515 x 50001 bf16 20 us; loss and gradient of 2048 x 128256
-// bf16, record of 128, 245 us (4.3 TB/s read and written), 37 x 32001 float32 11 us.
+// gradient), which two other CTAs on the SM cover in part, and 17.6 instructions a logit, the row's fixed part among
+// them.  Measured: the loss of 2304 x 128256 bf16, record of 64, 99.6 us (5.95 TB/s), 515 x 50001 bf16 21.8 us with the
+// host's call; loss and gradient of 2048 x 128256 bf16, record of 128, 236 us (4.5 TB/s read and written), 37 x 32001
+// float32 18 to 22 us with the host's call.
 template <typename T, bool kGrad>
 __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kernel(const __grid_constant__ DistillParams p) {
   extern __shared__ __align__(16) unsigned char raw[];

@@ -1480,9 +1480,9 @@ __device__ void scan_row(const T* row, int V, const Slice& s, Shared& sh) {
 // The batch, a cluster of CTAs per row.  Bound: for many rows DRAM while they stream (four CTAs
 // per SM with 64 KB of loads in flight together), then the chain of barriers of a row's list (some 25000 cycles: gather, weights, cut, draw), which
 // the SM's other rows cover, and the second pass of the last rows, which nothing covers (130000 to 200000 cycles).
-// Measured: 1280 x 152064 float32, top-p 0.9 to 0.95, 303 to 358 us (2.2 to 2.6 TB/s; one row in twenty takes a second
+// Measured: 1280 x 152064 float32, top-p 0.9 to 0.95, 303 to 360 us (2.2 to 2.6 TB/s; one row in twenty takes a second
 // pass; 196 us, 4.0 TB/s, where none does); the same rows with top-k and top-p 196 us; 64 x 128256 bf16 with mixed
-// filters 46 us; 333 x 50001 float32, min-p, 32.6 us; 8 x 32128 bf16 16 us.
+// filters 43 to 59 us; 333 x 50001 float32, min-p, 33.4 us; 8 x 32128 bf16 16 us.
 template <typename T>
 __global__ void __launch_bounds__(kFT, 4) sample_filtered_kernel(FilterParams q) {
   extern __shared__ __align__(16) unsigned char raw[];
@@ -1729,7 +1729,7 @@ __device__ void top_from_row(const T* row, int V, float M, int K, Shared& sh, fl
 
 // The K largest logits from the list (ranked by counting for up to kFT of them, sorted beyond) and the log-sum-exp from
 // the list's exact weights and the stream's float32 sum of the rest.  Bound as above.  Measured: top 64 of 1536 x
-// 152064 float32 206 us (4.5 TB/s; 6 TB/s while the rows stream); top 20 of 5 x 32000 12.9 us.
+// 152064 float32 209 us (4.5 TB/s; 6 TB/s while the rows stream); top 20 of 5 x 32000 12.9 us.
 template <typename T>
 __global__ void __launch_bounds__(kFT, 4) top_logits_kernel(TopParams q) {
   extern __shared__ __align__(16) unsigned char raw[];
