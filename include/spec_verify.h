@@ -286,7 +286,8 @@ int spec_sample_rows_masked(const void* logits, int dtype, const float* uniforms
 /* The draft-side sampler with a request's own parameters: temperature, top-k,
  * top-p and min-p per row, and one given uniform number.  For each row r of
  * `logits`, with M its largest logit, T = temperature[r] and the weights
- * w(x) = exp((l(x) - M) / T) (0 below e^-87), the kept tokens are
+ * w(x) = exp((l(x) - M) / T) (0 below e^-87, give or take 10^-5 of the exponent),
+ * the kept tokens are
  *   top-k:  k = top_k[r] > 0: the logits at or above the k-th largest (k = 0 or k >= V: all),
  *   top-p:  p = top_p[r] < 1: of those, the shortest descending run whose weight
  *           reaches p times their sum (p = 1: all),
@@ -350,11 +351,11 @@ int spec_top_logits(const void* logits, int dtype, float temperature, int R, int
  *    beyond the record, r = max(0, 1 - sum p_i), is one more outcome, compared with the student's mass
  *    outside the record: loss = sum_i p_i ln(p_i / q_i) + r ln(r / Q_rest).  An r of at most
  *    2^-21 (1 + |lse|), which the rounding of lse leaves where the record holds all that the teacher gives
- *    mass to (a constrained vocabulary, K = V), counts as 0 where the student too has less than e^-87 of
- *    its mass beyond the record.
+ *    mass to (a constrained vocabulary, K = V), counts as 0 where the student too has less than some e^-87
+ *    of its mass beyond the record (V tokens of e^-87 of its largest at most).
  *  - teacher_lse NULL: p is the softmax of the record's values / T, and loss = sum_i p_i ln(p_i / q_i).
  * A term with p_i = 0 (or r = 0) is 0; a token with p_i > 0 whose student logit
- * is -inf makes the loss +inf.  Sums are float32, compensated; those over the
+ * is -inf makes the loss +inf, and so may one of -1e38 and less.  Sums are float32, compensated; those over the
  * record's tokens and over the others are taken apart however far their logits
  * lie from one another, and in each a weight more than 87 below the largest in the
  * logarithm (logits 87 T apart) may count as 0.
@@ -366,7 +367,7 @@ int spec_top_logits(const void* logits, int dtype, float temperature, int R, int
  *   loss       [N]     float32 out
  *   stats      [N, 2]  float32 out of the forward pass, in of the backward pass: the log-sum-exp of
  *                      student / T over the vocabulary, and over the tokens outside the record (which may be
- *                      -inf where those hold less than e^-87 of the whole and the teacher's r is 0)
+ *                      -inf where none of those has e^-87 of the largest and the teacher's r is 0)
  *   grad_loss  [N]     float32: dL/dloss; NULL: 1 for every row
  *   grad       [N, V]  dtype, out: grad_loss[n] * dloss[n]/dstudent[n, :], rounded once; it may not overlap
  *                      student

@@ -345,7 +345,9 @@ __device__ Pair sum_slice(const T* row, int V, const Slice<T>& s, const uint32_t
     }
   }
   auto one = [&](int id, int bit) {
-    if (!((bits[bit >> 5] >> (bit & 31)) & 1u)) sum.lo += w(Elems<T>::one(row, id));
+    if ((bits[bit >> 5] >> (bit & 31)) & 1u) return;
+    const Pair t = two_sum(sum.hi, w(Elems<T>::one(row, id)));
+    sum = Pair{t.hi, sum.lo + t.lo};
   };
   if (s.first && tid < s.head) one(tid, s.per * kV + tid);
   if (s.last && tid < V - s.head - s.nv * kV) one(s.head + s.nv * kV + tid, s.per * kV + 8 + tid);

@@ -87,10 +87,10 @@ def check(S, student, v, i, T, lse, rows=None, stats=None):
         terms = (p[some] * (np.abs(np.log(p[some])) + np.abs(far[some]))).sum()
         tl = 3 * a + 8 * HALF * terms + r * 2 * a + r_off * (log_r + gap + 2) + 8 * HALF * r * (log_r + gap)
         for x in (loss[n].item(), loss2[n].item()):
-            assert x == L or (L > most * (1 - HALF) and x == np.inf) or abs(x - L) <= tl + HALF * min(L, most), (n, x, L, tl)
+            assert x == L or (L > 1e38 and x == np.inf) or abs(x - L) <= tl + HALF * min(L, most), (n, x, L, tl)
         got = st[n].tolist()
         for x, y in zip(got, w["stats"]):
-            nothing = y < -most or (r == 0 and w["gap"] > 87 and y == w["stats"][1])
+            nothing = y < -most or (r == 0 and w["gap"] > 87.5 - np.log(V) and y == w["stats"][1])
             assert x == y or (nothing and x == -np.inf) or abs(x - y) <= a + HALF * abs(y), (n, got, w["stats"])
         rel = lambda x: 2 * a + 6 * HALF * np.where(np.isfinite(x), np.abs(x), 0.0) + 2.0 ** -20  # noqa: E731
         for k, x in enumerate((grad, grad2)):
@@ -272,3 +272,21 @@ def test_logits_far_from_zero(S, N, V, shift):
     student, v, i, lse = batch(N, V, 25, "f32", 1.0, 66)
     for l in (lse, None):
         check(S, student + shift, v, i, 1.0, l, [0, N - 1])
+
+
+@pytest.mark.parametrize("V", [1, 2, 3, 5, 9, 17, 1402])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shift", [0.0, 2992.0, -1e4])
+def test_rows_whose_weight_lies_in_their_ends(S, V, dtype, shift):
+    # the logits outside a row's 16-byte aligned body: a short row's all, a rising row's largest
+    N = 40
+    g = torch.Generator(device="cuda").manual_seed(V)
+    t = torch.float32 if dtype == "f32" else torch.bfloat16
+    for T in (1.0, 0.3):
+        x = torch.sort(3 * torch.randn(N, V, device="cuda", generator=g), dim=1).values + shift
+        buf = torch.empty(N * V + 3, device="cuda", dtype=t)
+        for at in (0, 1, 3):  # (the ends differ from row to row where V is odd)
+            student = buf[at:at + N * V].view(N, V).copy_(x)
+            values, ids, lse = S.top_logits(2 * torch.randn(N, V, device="cuda", generator=g), 1, T)
+            check(S, student, values, ids, T, None)
+            check(S, student, values, ids, T, lse + 0.2)
