@@ -351,8 +351,8 @@ int spec_top_logits(const void* logits, int dtype, float temperature, int R, int
  *    beyond the record, r = max(0, 1 - sum p_i), is one more outcome, compared with the student's mass
  *    outside the record: loss = sum_i p_i ln(p_i / q_i) + r ln(r / Q_rest).  An r of at most
  *    2^-21 (1 + |lse|), which the rounding of lse leaves where the record holds all that the teacher gives
- *    mass to (a constrained vocabulary, K = V), counts as 0 where the student too has less than some e^-87
- *    of its mass beyond the record (V tokens of e^-87 of its largest at most).
+ *    mass to (a constrained vocabulary, K = V), counts as 0 where the student too has less than e^-60 of
+ *    its mass beyond the record.
  *  - teacher_lse NULL: p is the softmax of the record's values / T, and loss = sum_i p_i ln(p_i / q_i).
  * A term with p_i = 0 (or r = 0) is 0; a token with p_i > 0 whose student logit
  * is -inf makes the loss +inf, and so may one of -1e38 and less.  Sums are float32, compensated; those over the
@@ -367,7 +367,7 @@ int spec_top_logits(const void* logits, int dtype, float temperature, int R, int
  *   loss       [N]     float32 out
  *   stats      [N, 2]  float32 out of the forward pass, in of the backward pass: the log-sum-exp of
  *                      student / T over the vocabulary, and over the tokens outside the record (which may be
- *                      -inf where none of those has e^-87 of the largest and the teacher's r is 0)
+ *                      -inf where those hold less than e^-60 of the whole and the teacher's r is 0)
  *   grad_loss  [N]     float32: dL/dloss; NULL: 1 for every row
  *   grad       [N, V]  dtype, out: grad_loss[n] * dloss[n]/dstudent[n, :], rounded once; it may not overlap
  *                      student
