@@ -286,8 +286,8 @@ int spec_sample_rows_masked(const void* logits, int dtype, const float* uniforms
 /* The draft-side sampler with a request's own parameters: temperature, top-k,
  * top-p and min-p per row, and one given uniform number.  For each row r of
  * `logits`, with M its largest logit, T = temperature[r] and the weights
- * w(x) = exp((l(x) - M) / T) (0 below e^-87, give or take 10^-5 of the exponent),
- * the kept tokens are
+ * w(x) = exp((l(x) - M) / T) (0 below e^-87.00002 and not before e^-87), the kept
+ * tokens are
  *   top-k:  k = top_k[r] > 0: the logits at or above the k-th largest (k = 0 or k >= V: all),
  *   top-p:  p = top_p[r] < 1: of those, the shortest descending run whose weight
  *           reaches p times their sum (p = 1: all),

@@ -762,7 +762,8 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
       bool redo = __any_sync(0xffffffffu, far);
       if (!(rest >= kLeastRest)) {
         // no weight outside the record at all, less than V 2^-126 to the record's 2^-20 (e^-60 and less): nothing to know
-        // of it where the teacher has no mass there either (both models' vocabularies constrained alike: 2304 x 128256 bf16 108 us, 238 with a second pass)
+        // of it where the teacher has no mass there either (both models' vocabularies constrained alike: 2304 x 128256
+        // bf16 108 us, 238 with a second pass)
         Pair mass{0.f, 0.f};
         float top = 0.f;
 #pragma unroll 1

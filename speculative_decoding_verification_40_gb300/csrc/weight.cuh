@@ -18,7 +18,9 @@ constexpr int kFixBits = 45;  // 2^18 weights of at most 1 sum to at most 2^63
 // ln(2) as the float32 nearest to it and the rest
 constexpr float kLn2Hi = 0.693147182464599609375f;
 constexpr float kLn2Lo = -1.904654299957767e-09f;
-constexpr float kLowestLog2 = -125.51346855f;  // -87 log2(e): weights below e^-87 are 0
+// -87 log2(e), and the roundings of its product with a scale below that: weights below e^-87 are 0, and one of e^-87 itself
+// (bfloat16 logits 21.75 apart at T = 1/4) is not
+constexpr float kLowestLog2 = -125.51449f;
 
 struct Exp2Table {
   float hi[64], lo[64];

@@ -149,3 +149,16 @@ def test_long_rows_at_extreme_temperatures_and_far_from_zero(S, R, T, shift):
         got = S.sample_filtered(x, u, *on_gpu(t, k, p, m))
         check(S, x[-few:], u[-few:], t[-few:], k[-few:], p[-few:], m[-few:], [y[-few:] for y in got])
     assert S.check_status() == 0
+
+
+@pytest.mark.parametrize("T,d", [(0.25, 21.75), (0.5, 43.5), (1.0, 87.0), (2.0, 174.0), (0.125, 10.875)])
+@pytest.mark.parametrize("n", [500, 20000])
+def test_a_weight_of_the_lowest_size_is_drawn_at_zero(S, n, T, d):
+    # at u = 0 the first token of any weight: e^-87 of the largest is one, the next logit below it is not
+    x = torch.full((2, n), -1e3, device="cuda")
+    x[:, 300], x[:, 5] = 25.0, 25.0 - d
+    x[:, 3] = torch.tensor([25.0 - d * 1.000001, -1e3], device="cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        y = x.to(dtype) if dtype == torch.float32 else x.to(dtype).index_fill(1, torch.tensor([3], device="cuda"), -1e3)
+        tokens = S.sample_filtered(y, torch.zeros(2, device="cuda"), T)[0].tolist()
+        assert tokens == [5, 5], (dtype, tokens)
