@@ -88,14 +88,32 @@ __device__ __forceinline__ float exp_pair(const Pair& x) {
   return fabsf(x.hi) < INFINITY ? __fmaf_rn(e, x.lo, e) : e;
 }
 
-// exp(x) of a pair, to some 2^-38 of itself: the teacher's mass beyond the record is what these leave of 1.
-__device__ __forceinline__ Pair probability(const Pair& x) {
-  const Pair y = x * Pair{1.44269502162933349609375f, 1.925963033500e-08f};
-  if (!(fabsf(y.hi) < 120.f)) return Pair{exp_pair(x), 0.f};
-  const float k = __fadd_rn(y.hi, 12582912.f);
-  const Pair e = exp2_near<false>(__fsub_rn(y.hi, __fsub_rn(k, 12582912.f))) * Pair{1.f, __fmul_rn(y.lo, kLn2Hi)};
-  const float scale = __int_as_float((127 + __float_as_int(k) - 0x4b400000) << 23);
-  return Pair{e.hi * scale, e.lo * scale};
+// exp(x) of a pair to some 2^-38 of itself, by the table and polynomial of weight.cuh: the teacher's mass beyond the
+// record is what these leave of 1.  In as few instructions as it takes, and only where there is a tail: short rows feel
+// every instruction that runs once (captured calls of 640 x 1307 float32, record of 8, the gradient: 7.5 us, 7.0 with
+// exp_pair; of 1614 x 1784 bf16, record of 44, the loss: 15.7, 15.5).
+__device__ __forceinline__ Pair tail_probability(Pair x, const float2* tab) {
+  const float y = __fmul_rn(x.hi, 1.44269502162933349609375f);
+  if (!(fabsf(y) < 120.f)) return Pair{exp_pair(x), 0.f};
+  const float yl = __fmaf_rn(x.hi, 1.44269502162933349609375f, -y) +
+                   __fmaf_rn(x.hi, 1.925963033500e-08f, __fmul_rn(x.lo, 1.44269502162933349609375f));
+  const float k = __fmaf_rn(y, 64.f, 12582912.f);  // y = (64 n + j) / 64 + s
+  const int m = __float_as_int(k) - 0x4b400000;
+  const float s = __fmaf_rn(__fsub_rn(k, 12582912.f), -0.015625f, y);
+  const float2 T = tab[m & 63];
+  const float t = __fmul_rn(s, kLn2Hi);  // 2^(s + yl) = 1 + t + p
+  const float tl = __fmaf_rn(s, kLn2Hi, -t) + __fmaf_rn(s, kLn2Lo, __fmul_rn(yl, kLn2Hi));
+  const float q = __fmul_rn(__fmul_rn(t, t), __fmaf_rn(t, __fmaf_rn(t, 1.f / 24.f, 1.f / 6.f), 0.5f));
+  const float p = __fadd_rn(__fmaf_rn(t, tl, tl), q);
+  const float a = __fmul_rn(T.x, t);  // (T.x + T.y) (1 + t + p)
+  const float rest = __fmaf_rn(T.x, t, -a) + __fmaf_rn(T.x, p, __fmaf_rn(T.y, t, T.y));
+  const Pair e = fast_two_sum(T.x, a);
+  const float scale = __int_as_float((127 + (m >> 6)) << 23);
+  return Pair{e.hi * scale, (e.lo + rest) * scale};
+}
+
+__device__ __forceinline__ Pair probability(const Pair& x, bool tail, const float2* tab) {
+  return tail ? tail_probability(x, tab) : Pair{exp_pair(x), 0.f};
 }
 
 // The teacher's mass beyond the record, given the record's, its log-sum-exp and how far the student's own mass there lies
@@ -205,6 +223,7 @@ struct __align__(8) Part {
 
 struct Shared {
   float red[kDW];
+  float2 tab[64];                    // for the record's probabilities
   Pair part[4][kDW];
   int count[kMaxTop / 32];
   Part parts[kDSplit];
@@ -236,7 +255,8 @@ __host__ __device__ inline int entry_bytes(int K) { return (K * static_cast<int>
 
 // exp(-x) of what the roundings of a scale miss: next to nothing but for logits of 10^4 T and more.
 __device__ __forceinline__ Pair make_up(float x) {
-  return fabsf(x) < 0.00195f ? Pair{1.f, __fmaf_rn(0.5f * x, x, -x)} : Pair{expf(-x), 0.f};
+  const bool little = fabsf(x) < 0.00195f;
+  return Pair{little ? 1.f : fast_exp2(-1.44269502f * x), little ? __fmaf_rn(0.5f * x, x, -x) : 0.f};
 }
 
 // Weights 2^(s c + shift), shift the float32 nearest to -ref c: one FFMA and one exponential a logit.  They stand
@@ -491,6 +511,21 @@ __device__ __noinline__ int own_references(const T* row, int V, const uint32_t* 
   return !(fabsf(most) < INFINITY) ? 0 : out > -INFINITY ? 2 : 1;
 }
 
+// Of a first pass without any weight outside the record (less than V 2^-126 to the record's 2^-20: e^-60 and less):
+// whether the teacher has no mass there either, so that nothing more has to be known (both models' vocabularies
+// constrained alike: 2304 x 128256 bf16 108 us, 238 with a second pass).
+__device__ __noinline__ bool nothing_beyond(const DistillParams& p, int r, const Shared& sh, int split, float most,
+                                            float c) {
+  Pair mass{0.f, 0.f};
+  float top = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < split; ++i) {
+    mass = mass + sh.parts[i].mass;
+    top += value(sh.parts[i].top) * step(sh.parts[i].ref, most, c);
+  }
+  return top >= 9.5367432e-7f && !(p.teacher_lse && beyond(mass, p.teacher_lse[r], INFINITY) > 0.f);
+}
+
 // The row's loss and statistics from its CTAs' parts, by one thread while the others go on to the gradient.  again: of
 // the second pass.
 __device__ __noinline__ void write_loss(const DistillParams& p, int r, const Shared& sh, int split, Pair inv_t, float c,
@@ -554,9 +589,11 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
   const float v0 = tid < p.K ? __ldg(values + tid) : 0.f;
   const float teacher_lse = p.teacher_lse ? __ldg(p.teacher_lse + r) : 0.f;
   const float g = kGrad && p.grad_loss ? __ldg(p.grad_loss + r) : 1.f;
+  const float2 entry = p.teacher_lse ? exp2_table_entry() : make_float2(0.f, 0.f);
   if (kGrad) keep_slice<T, kT>(row, s, kept);  // behind the loads above, which the row waits for first
   for (int i = tid; i < (bitmap_bytes(s.per, kV) + hit_bytes(s.per, kT)) / 16; i += kT)
     reinterpret_cast<uint4*>(bits)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < 64) sh.tab[tid] = entry;
   int some = id0 != -1;
   for (int k = tid + kT; k < p.K; k += kT) some |= ids[k] != -1;
   some = __syncthreads_or(some);
@@ -669,13 +706,13 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
         if (!index_ok(e.id >= 0 && e.id < p.V && i < p.K)) continue;
         if (again == 0) e.l = i < kT ? logit : Elems<T>::one(row, e.id);
         const Pair x = entry_log(rec, e.v);
-        const Pair pr = probability(x);
+        const Pair pr = probability(x, p.teacher_lse != nullptr, sh.tab);
         e.p = value(pr);
         if (again == 0) entries[i] = e;
         mass = mass + pr;
-        if (e.p > 0.f) {  // (p before 1 / T: a masked logit times 1 / T may leave float32's range)
+        if (e.p > 0.f) {
           if (e.l > -INFINITY)
-            against = against + (x * pr - two_sum(e.l, -ref) * pr * rec.inv_t);
+            against = against + (x - two_sum(e.l, -ref) * rec.inv_t) * e.p;
           else
             flags |= 2;
         }
@@ -760,20 +797,7 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
         }
       }
       bool redo = __any_sync(0xffffffffu, far);
-      if (!(rest >= kLeastRest)) {
-        // no weight outside the record at all, less than V 2^-126 to the record's 2^-20 (e^-60 and less): nothing to know
-        // of it where the teacher has no mass there either (both models' vocabularies constrained alike: 2304 x 128256
-        // bf16 108 us, 238 with a second pass)
-        Pair mass{0.f, 0.f};
-        float top = 0.f;
-#pragma unroll 1
-        for (int i = 0; i < split; ++i) {
-          mass = mass + sh.parts[i].mass;
-          top += value(sh.parts[i].top) * step(sh.parts[i].ref, most, c);
-        }
-        const float tail = p.teacher_lse ? beyond(mass, p.teacher_lse[r], INFINITY) : 0.f;
-        redo |= rest != 0.f || tail > 0.f || !(top >= 9.5367432e-7f);
-      }
+      if (!(rest >= kLeastRest)) redo |= rest != 0.f || !nothing_beyond(p, r, sh, split, most, c);
       if (lane == 0) {
         sh.most = most;
         sh.flags = any;
@@ -831,6 +855,7 @@ template <typename T>
 __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams p, int split) {
   __shared__ float red[kDW];
   __shared__ Pair part[kDW];
+  __shared__ float2 tab[64];
   const int r = blockIdx.x >> (__ffs(split) - 1), rank = blockIdx.x & (split - 1), tid = threadIdx.x;
   const T* row = static_cast<const T*>(p.student) + static_cast<size_t>(r) * p.V;
   T* out = static_cast<T*>(p.grad) + static_cast<size_t>(r) * p.V;
@@ -849,6 +874,7 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   };
   const float teacher_lse = p.teacher_lse ? p.teacher_lse[r] : 0.f;
   const float lse = p.stats[2 * r], lse_rest = p.stats[2 * r + 1];
+  if (p.teacher_lse && tid < 64) tab[tid] = exp2_table_entry();
   int some = 0, bad = 0;
   if (g != 0.f)
     for (int k = tid; k < p.K; k += kDT) {
@@ -865,7 +891,7 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   const Record rec = read_record<kDT>(p, r, teacher_lse, red, part, &bad);
   Pair mass{0.f, 0.f};
   for (int k = tid; k < p.K; k += kDT)
-    if (ids[k] >= 0 && values[k] > -INFINITY) mass = mass + probability(entry_log(rec, values[k]));
+    if (ids[k] >= 0 && values[k] > -INFINITY) mass = mass + probability(entry_log(rec, values[k]), p.teacher_lse != nullptr, tab);
   mass = block_sum<kDT>(mass, part);
   bad |= !(fabsf(lse) < kTelling);  // the forward pass found the row invalid, or its statistics tell nothing
   bad = __syncthreads_or(bad);
@@ -882,13 +908,21 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   };
   // tokens outside the record: q less their share of the tail, relative to lse, or to lse_rest where that is so far
   // below that q is nothing and the quotient of the two would leave float32's range
-  const bool apart = gap > 40.f && fabsf(lse_rest) < kTelling;
-  const float ratio = exp_pair(two_sum(apart ? lse_rest : lse, apart ? -lse : -lse_rest));
-  const float share = tail > 0.f && fabsf(lse_rest) < kTelling ? tail * (apart ? 1.f : ratio) : 0.f;
-  float k_in, k;
-  const Scale w_in = scale_of(lse, k_in), w = scale_of(apart ? lse_rest : lse, k);
+  float k_in;
+  const Scale w_in = scale_of(lse, k_in);
+  Scale w = w_in;
+  float k_out;
+  if (__builtin_expect(gap > 40.f && fabsf(lse_rest) < kTelling, 0)) {
+    float k;
+    w = scale_of(lse_rest, k);
+    k_out = (both * exp_pair(two_sum(lse_rest, -lse)) - tail) * k;
+  } else {
+    const float share =
+        tail > 0.f && fabsf(lse_rest) < kTelling ? tail * exp_pair(two_sum(lse, -lse_rest)) : 0.f;
+    k_out = (both - share) * k_in;
+  }
   k_in *= both;
-  const float k_out = bad ? NAN : (both * (apart ? ratio : 1.f) - share) * k;
+  if (bad) k_out = NAN;
   T* body = out + s.head;
   const bool vec = p.vec != 0;
   while (v < s.v1) {
@@ -904,7 +938,7 @@ __global__ void __launch_bounds__(kDT, 4) distill_backward_kernel(DistillParams 
   for (int k = tid; k < p.K; k += kDT) {  // the slice's tokens of the record, over what was written there
     const int id = ids[k];
     if (id < 0 || s.bit(id) < 0 || !index_ok(id < p.V)) continue;
-    const float pk = values[k] > -INFINITY ? value(probability(entry_log(rec, values[k]))) : 0.f;
+    const float pk = values[k] > -INFINITY ? exp_pair(entry_log(rec, values[k])) : 0.f;
     out[id] = to_grad<T>(__fmaf_rn(w_in(Elems<T>::one(row, id)), k_in, -__fmul_rn(pk, scale)));
   }
 }

@@ -51,23 +51,23 @@ __device__ __forceinline__ Pair warp_sum(Pair v) {
   return v;
 }
 
-// 2^y for |y| <= 0.51 to 2^-40, by the table and polynomial of weight.cuh.  kOne: called by one thread of a warp, the
-// table in constant memory (which serves one address at a time); else in global memory.
-template <bool kOne>
-__device__ __forceinline__ Pair exp2_near(float y) {
+// 2^y for |y| <= 0.51 to 2^-40, by the table (entry(j), j < 64) and polynomial of weight.cuh.
+template <typename F>
+__device__ __forceinline__ Pair exp2_near(float y, F&& entry) {
   const float k = __fmaf_rn(y, 64.f, 12582912.f);
   const int m = __float_as_int(k) - 0x4b400000;
   const float s = __fmaf_rn(__fsub_rn(k, 12582912.f), -0.015625f, y);
   const float scale = m < 0 ? 0.5f : 1.f;  // m in [-33, 33]
-  const Exp2Table& tab = kOne ? kExp2Table : kExp2TableGlobal;
-  const Pair T{tab.hi[m & 63] * scale, tab.lo[m & 63] * scale};
+  const float2 t64 = entry(m & 63);
+  const Pair T{t64.x * scale, t64.y * scale};
   const float t = __fmul_rn(s, kLn2Hi);
   const float tl = __fmaf_rn(s, kLn2Hi, -t) + __fmul_rn(s, kLn2Lo);
   const float q = __fmul_rn(__fmul_rn(t, t), __fmaf_rn(t, __fmaf_rn(t, 1.f / 24.f, 1.f / 6.f), 0.5f));
   return T + T * Pair{t, __fadd_rn(tl, q)};
 }
 
-// ln(s) of a positive normal s: s = 2^n f with f in [0.707, 1.414); y = log2(f) in float32, and what it misses,
+// ln(s) of a positive normal s, by one thread of a warp (the table in constant memory, which serves one address at a
+// time): s = 2^n f with f in [0.707, 1.414); y = log2(f) in float32, and what it misses,
 // ln(f 2^-y) = d - d^2 / 2 with d = f 2^-y - 1 below 2^-21.
 __device__ __forceinline__ Pair log_pair(const Pair& s) {
   const int n = ((__float_as_int(s.hi) - 0x3f3504f3) >> 23);
@@ -75,7 +75,7 @@ __device__ __forceinline__ Pair log_pair(const Pair& s) {
   const float down1 = __int_as_float((127 - n / 2) << 23), down2 = __int_as_float((127 - (n - n / 2)) << 23);
   const Pair f{s.hi * down1 * down2, s.lo * down1 * down2};
   const float y = log2f(f.hi);
-  const Pair d = f * exp2_near<true>(-y) - Pair{1.f, 0.f};
+  const Pair d = f * exp2_near(-y, [](int j) { return make_float2(kExp2Table.hi[j], kExp2Table.lo[j]); }) - Pair{1.f, 0.f};
   const float miss = __fadd_rn(d.hi, __fadd_rn(d.lo, -0.5f * d.hi * d.hi));
   return Pair{kLn2Hi, kLn2Lo} * static_cast<float>(n) + (Pair{kLn2Hi, kLn2Lo} * y + Pair{miss, 0.f});
 }
