@@ -710,9 +710,9 @@ __global__ void __launch_bounds__(threads_of(kGrad), kGrad ? 3 : 8) distill_kern
         e.p = value(pr);
         if (again == 0) entries[i] = e;
         mass = mass + pr;
-        if (e.p > 0.f) {
+        if (e.p > 0.f) {  // (p before 1 / T: a masked logit times 1 / T may leave float32's range)
           if (e.l > -INFINITY)
-            against = against + (x - two_sum(e.l, -ref) * rec.inv_t) * e.p;
+            against = against + (x * pr - two_sum(e.l, -ref) * pr * rec.inv_t);
           else
             flags |= 2;
         }

@@ -5,7 +5,7 @@ Tolerances.  A log-sum-exp is within a(V) = (V/256 + 84) 2^-24 of its value (tes
 x from the largest of its kind (in nats) carries x 2^-24 from the scale's rounding, its own and that of the step
 between two references, the hardware exponential's 2^-22, and a factor's few roundings: rel(x) = 2 a + 6 x 2^-24 +
 2^-20.  The record's probabilities are kept to 2^-38 (1 + |lse| / 8): so is r = 1 - sum p, before one rounding; in a
-gradient p / T takes three more (p's own, 1 / T's and the product's, half a step of 2^-23 each).  The
+gradient p / T is within 2^-23 of p for expf (documented: one step), and three times 2^-24 (p's own rest, 1 / T, the product).  The
 loss adds p (ln p - z + lse) and r (ln r - lse_rest + lse), pairs of float32 until the last rounding.  The backward
 pass takes both log-sum-exps from float32: 2 steps of 2^-24 of their size more.  Weights below 2^-126 of the largest of
 the pass's reference are 0, which is at least 2^-60 of what they are divided by.
@@ -97,7 +97,7 @@ def check(S, student, v, i, T, lse, rows=None, stats=None):
         for k, x in enumerate((grad, grad2)):
             held = 2 * HALF * np.abs(w["stats"][0 if r == 0 or np.isinf(gap) else [0, 1]]).sum() if k == 0 else 0.0
             tg = (w["q"] * (p.sum() + r) * (rel(far) + held) + w["out"] * (r * (rel(w["far_out"]) + held) + r_off) +
-                  3 * HALF * p + 2.0 ** -60 * (p.sum() + r)) / T + eps / 2 * np.abs(G) + 2.0 ** -126
+                  5 * HALF * p + 2.0 ** -60 * (p.sum() + r)) / T + eps / 2 * np.abs(G) + 2.0 ** -126
             y = F.rows64(x[n])
             if k == 0 and abs(w["stats"][0]) >= 2.0 ** 22:  # float32 statistics that tell no weights
                 assert np.isnan(y).all()
@@ -307,3 +307,16 @@ def test_weights_that_only_the_first_reference_hides(S, dtype):
             check(S, s, v, i, T, None)
             check(S, s, v, i, T, (v[:, 0].double() / T + 0.01).float())
             check(S, s, v, i, T, (v[:, 0] / T).clone())
+
+
+@ROWS
+@pytest.mark.parametrize("T", [0.01, 0.25, 0.7, 1.0])
+def test_next_to_no_mass_on_a_masked_token(S, N, V, T):
+    # p of e^-60 to e^-85 on tokens that the student masks by the type's lowest value: p times 3.4e38 / T is what counts
+    student, v, i, _ = batch(N, V, 8, "f32", T, 68)
+    v = (torch.tensor([0.0, -0.1, -0.5, -60.0, -70.0, -80.0, -84.0, -85.0], device="cuda") * T).repeat(N, 1)
+    lse = torch.logsumexp(v.double() / T, 1).float()
+    for first in (3, 5, 7):
+        x = student.clone().scatter_(1, i[:, first:].long(), MIN)
+        for l in (lse, None):
+            check(S, x, v, i, T, l, [0, N - 1])
